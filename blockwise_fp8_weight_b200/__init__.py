@@ -14,6 +14,16 @@ pages' Python API (verl docs "fp8_kernel.py -- FP8 量化内核", section 1 and
     scaled_fp8_blockwise(data_hp, weight_block_size) -> (fp8_data, descale)
     quant_weights(named_weights, weight_block_size)  -> [(name, fp8), (name + "_scale_inv", s), ...]
 
+and the same for microscaled 4-bit floating point ("mxfp4", "nvfp4"), with the
+products that read it:
+
+    scaled_fp4_blockwise(data_hp, format)            -> (codes, scales)
+    quant_weights_fp4(named_weights, format)         -> [(name, codes), (name + "_scale", s), ...]
+    dequantize_fp4_blockwise(codes, scales, format)  -> values
+    matmul_fp4(a, a_scales, b, b_scales, format)     -> a b^T
+    gated_matmul_fp4(a, a_scales, gate, gate_scales, up, up_scales, format)
+                                                     -> silu(a gate^T) * (a up^T)
+
 They allocate the outputs with PyTorch (device memory and streams are
 PyTorch's job here) and hand the pointers to the library.
 
@@ -26,6 +36,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Iterable, Sequence
 
@@ -56,6 +67,9 @@ FP8BQ_PATH_TMA = 2
 FP8BQ_PATH_GENERIC = 3
 FP8BQ_INJECT_DROP_FIRST_LOAD = 1
 FP8BQ_INJECT_TRIM_OUTPUTS = 2
+# fp8bq_fp4_format
+FP8BQ_MXFP4 = 0
+FP8BQ_NVFP4 = 1
 
 DEFAULT_BLOCK = (128, 128)
 
@@ -96,6 +110,38 @@ class fp8bq_scale_desc(ctypes.Structure):
     """Mirror of ``struct fp8bq_scale_desc`` (24 bytes)."""
     _fields_ = [("x", ctypes.c_void_p), ("numel", ctypes.c_int64),
                 ("dtype_in", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class fp8bq_fp4_desc(ctypes.Structure):
+    """Mirror of ``struct fp8bq_fp4_desc`` (88 bytes)."""
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+        ("tensor_scale", ctypes.c_void_p),
+        ("M", ctypes.c_int64), ("K", ctypes.c_int64), ("ld", ctypes.c_int64),
+        ("batch", ctypes.c_int64), ("x_batch_stride", ctypes.c_int64),
+        ("tensor_scale_stride", ctypes.c_int64),
+        ("dtype_in", ctypes.c_int32), ("format", ctypes.c_int32),
+    ]
+
+
+class fp8bq_fp4_operand(ctypes.Structure):
+    """Mirror of ``struct fp8bq_fp4_operand`` (48 bytes)."""
+    _fields_ = [
+        ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("tensor_scale", ctypes.c_void_p),
+        ("codes_batch_stride", ctypes.c_int64), ("scales_batch_stride", ctypes.c_int64),
+        ("tensor_scale_stride", ctypes.c_int64),
+    ]
+
+
+class fp8bq_fp4_matmul_desc(ctypes.Structure):
+    """Mirror of ``struct fp8bq_fp4_matmul_desc`` (216 bytes)."""
+    _fields_ = [
+        ("a", fp8bq_fp4_operand), ("b", fp8bq_fp4_operand), ("up", fp8bq_fp4_operand),
+        ("out", ctypes.c_void_p), ("rows", ctypes.c_void_p),
+        ("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("batch", ctypes.c_int64), ("ld_out", ctypes.c_int64), ("out_batch_stride", ctypes.c_int64),
+        ("format", ctypes.c_int32), ("dtype_out", ctypes.c_int32),
+    ]
 
 
 class Fp8bqError(RuntimeError):
@@ -158,6 +204,18 @@ def lib() -> ctypes.CDLL:
             L.fp8bq_debug_take_bounds.argtypes = [ctypes.POINTER(ctypes.c_uint64),
                                                   ctypes.POINTER(ctypes.c_uint64)]
             L.fp8bq_debug_take_bounds.restype = i32
+            L.fp8bq_fp4_quantize.argtypes = [vp, i32, i64, i64, i64, i32, vp, vp, vp, vp]
+            L.fp8bq_fp4_quantize.restype = i32
+            L.fp8bq_fp4_quantize_batched.argtypes = [vp, i32, vp]
+            L.fp8bq_fp4_quantize_batched.restype = i32
+            L.fp8bq_fp4_dequantize.argtypes = [vp, vp, i64, i64, i64, i32, vp, i64, vp, i32, i64,
+                                               i64, vp]
+            L.fp8bq_fp4_dequantize.restype = i32
+            # the descriptor: a fp8bq_fp4_matmul_desc by reference, or its bytes
+            L.fp8bq_fp4_matmul.argtypes = [vp, vp]
+            L.fp8bq_fp4_matmul.restype = i32
+            L.fp8bq_fp4_gated_matmul.argtypes = [vp, vp]
+            L.fp8bq_fp4_gated_matmul.restype = i32
             _lib = L
     return _lib
 
@@ -224,6 +282,40 @@ def fp8bq_tensor_scale(desc_table, scale_out, n_tensors=None, stream=None) -> in
         desc_table = (fp8bq_scale_desc * len(desc_table))(*desc_table)
     n = len(desc_table) if n_tensors is None else n_tensors
     return lib().fp8bq_tensor_scale(desc_table, n, _ptr(scale_out), _stream(stream))
+
+
+def fp8bq_fp4_quantize(x, dtype_in: int, M: int, K: int, ld: int, format: int, tensor_scale, codes,
+                       scales, stream=None) -> int:
+    """``fp8bq_fp4_quantize`` of the C ABI.  Returns the status code."""
+    return lib().fp8bq_fp4_quantize(_ptr(x), dtype_in, M, K, ld, format, _ptr(tensor_scale),
+                                    _ptr(codes), _ptr(scales), _stream(stream))
+
+
+def fp8bq_fp4_quantize_batched(desc_table, n_tensors=None, stream=None) -> int:
+    """``fp8bq_fp4_quantize_batched`` of the C ABI.  Returns the status code."""
+    if not isinstance(desc_table, ctypes.Array):
+        desc_table = (fp8bq_fp4_desc * len(desc_table))(*desc_table)
+    n = len(desc_table) if n_tensors is None else n_tensors
+    return lib().fp8bq_fp4_quantize_batched(desc_table, n, _stream(stream))
+
+
+def fp8bq_fp4_dequantize(codes, scales, batch: int, M: int, K: int, format: int, tensor_scale,
+                         tensor_scale_stride: int, out, dtype_out: int, ld_out: int,
+                         out_batch_stride: int, stream=None) -> int:
+    """``fp8bq_fp4_dequantize`` of the C ABI.  Returns the status code."""
+    return lib().fp8bq_fp4_dequantize(_ptr(codes), _ptr(scales), batch, M, K, format,
+                                      _ptr(tensor_scale), tensor_scale_stride, _ptr(out),
+                                      dtype_out, ld_out, out_batch_stride, _stream(stream))
+
+
+def fp8bq_fp4_matmul(desc: fp8bq_fp4_matmul_desc, stream=None) -> int:
+    """``fp8bq_fp4_matmul`` of the C ABI.  Returns the status code."""
+    return lib().fp8bq_fp4_matmul(ctypes.byref(desc), _stream(stream))
+
+
+def fp8bq_fp4_gated_matmul(desc: fp8bq_fp4_matmul_desc, stream=None) -> int:
+    """``fp8bq_fp4_gated_matmul`` of the C ABI.  Returns the status code."""
+    return lib().fp8bq_fp4_gated_matmul(ctypes.byref(desc), _stream(stream))
 
 
 def fp8bq_status_string(status: int) -> str:
@@ -505,3 +597,269 @@ def quant_weights(weights: Iterable, weight_block_size=DEFAULT_BLOCK, stream=Non
                                       len(named), _stream(stream))
     check(st, "quant_weights")
     return out
+
+
+# ----------------------------------------------------------------- 4-bit conveniences
+
+_FP4_FORMATS = {"mxfp4": (FP8BQ_MXFP4, 32), "nvfp4": (FP8BQ_NVFP4, 16)}
+
+
+def _fp4_format(format: str) -> tuple[int, int]:
+    """(fp8bq_fp4_format, values a scale) of a format's name."""
+    try:
+        return _FP4_FORMATS[format]
+    except (KeyError, TypeError):
+        raise ValueError(f"format must be 'mxfp4' or 'nvfp4', got {format!r}") from None
+
+
+def _fp4_tensor_scale(t, batch: int, format: str, what: str) -> tuple[int, int]:
+    """(pointer, stride) of a tensor scale: None, one fp32 value, or one for
+    each matrix of a stack."""
+    if t is None:
+        return 0, 0
+    import torch
+    _check_cuda(t, what)
+    if format == "mxfp4":
+        raise ValueError(f"{what}: mxfp4 has no tensor scale")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{what} must be float32, got {t.dtype}")
+    n = t.numel()
+    if n != 1 and n != batch:
+        raise ValueError(f"{what} must hold one value, or one for each of the {batch} matrices")
+    if n > 1 and not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr(), int(n > 1)
+
+
+def _fp4_shapes(x, block: int):
+    """Shapes of the codes and of the scale tiles of ``x``."""
+    M, K = x.shape[-2], x.shape[-1]
+    return ((*x.shape[:-1], 16 * (-(-K // 32))),
+            (*x.shape[:-2], -(-M // 128), -(-K // (4 * block)), 32, 16))
+
+
+def _fp4_record(w, name: str, format: str, codes: int, scales: int, tensor_scale):
+    """The fields of an ``fp8bq_fp4_desc`` for the tensor ``w``."""
+    _check_cuda(w, name)
+    if w.dim() not in (2, 3):
+        raise ValueError(f"{name}: expected a 2-D weight or a 3-D stack of expert weights")
+    M, K = w.shape[-2], w.shape[-1]
+    if K > 1 and w.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension of the input must have unit stride")
+    stack = w.dim() == 3
+    E = w.shape[0] if stack else 1
+    t, ts = _fp4_tensor_scale(tensor_scale, E, format, f"{name}'s tensor scale")
+    return (w.data_ptr(), codes, scales, t, M, K, max(w.stride(-2) if M > 1 else K, K), E,
+            w.stride(0) if stack else 0, ts, _dtype_code(w), _FP4_FORMATS[format][0])
+
+
+def scaled_fp4_blockwise(data_hp, format="mxfp4", tensor_scale=None, stream=None):
+    """Quantize one bf16/fp32 CUDA tensor ([M, K], or [E, M, K] for a stack) to
+    4 bits: ``"mxfp4"`` (a power-of-two scale for each 32 values of a row) or
+    ``"nvfp4"`` (an e4m3 scale for each 16, times ``tensor_scale``, an fp32 CUDA
+    tensor of one value or of one for each matrix of the stack; None is 1).
+
+    Returns ``(codes, scales)``, both uint8: codes [(E,) M, 16 * ceil(K / 32)],
+    two e2m1 codes a byte; scales [(E,) ceil(M / 128), ceil(K / 4B), 32, 16], B
+    the block length, in the tiles that the products read (``fp4_scale_rows``
+    gives them row by row).  Both are padded with zeros.
+    """
+    import torch
+    fmt, block = _fp4_format(format)
+    _check_cuda(data_hp, "data_hp")
+    if data_hp.dim() not in (2, 3):
+        raise ValueError("expected a 2-D weight or a 3-D stack of expert weights")
+    cs, ss = _fp4_shapes(data_hp, block)
+    with _on_stream(stream):
+        codes = torch.empty(cs, dtype=torch.uint8, device=data_hp.device)
+        scales = torch.empty(ss, dtype=torch.uint8, device=data_hp.device)
+    rec = _fp4_record(data_hp, "data_hp", format, codes.data_ptr(), scales.data_ptr(), tensor_scale)
+    check(lib().fp8bq_fp4_quantize_batched(_FP4_DESC.pack(*rec), 1, _stream(stream)),
+          "scaled_fp4_blockwise")
+    return codes, scales
+
+
+# fp8bq_fp4_desc and fp8bq_fp4_matmul_desc as packed bytes: one call of the
+# struct module instead of a field at a time.
+_FP4_DESC = struct.Struct("<4Q6q2i")
+_FP4_MATMUL_DESC = struct.Struct("<" + 3 * "3Q3q" + "2Q6q2i")
+
+
+def fp4_scale_rows(scales, rows: int, columns: int, format="mxfp4"):
+    """The scale bytes of ``scaled_fp4_blockwise`` as [(E,) rows, ceil(columns / B)],
+    the order of a checkpoint (a copy)."""
+    _, block = _fp4_format(format)
+    mt, kt = scales.shape[-4], scales.shape[-3]
+    s = scales.reshape(*scales.shape[:-2], 32, 4, 4).movedim(-4, -2).movedim(-4, -3)
+    return s.reshape(*s.shape[:-5], mt * 128, kt * 4)[..., :rows, :-(-columns // block)].contiguous()
+
+
+def quant_weights_fp4(weights: Iterable, format="mxfp4", stream=None):
+    """Quantize every (name, tensor) pair to 4 bits in one grouped call and
+    return the list a rollout engine loads: (name, codes), (name + "_scale",
+    scales) and, for ``"nvfp4"``, (name + "_scale_2", tensor scale) for each
+    input, in input order.  The tensor scale is max(max|w|, eps) / (448 * 6),
+    so that the largest block's scale is 448."""
+    import torch
+    fmt, block = _fp4_format(format)
+    named = list(weights)
+    if not named:
+        return []
+    for name, w in named:
+        _check_cuda(w, name)
+        if w.dim() not in (2, 3):
+            raise ValueError(f"{name}: expected a 2-D weight or a 3-D stack of expert weights")
+    shapes = [_fp4_shapes(w, block) for _, w in named]
+    with _on_stream(stream):
+        ts = None
+        if format == "nvfp4":
+            ts = tensor_scales([w if w.is_contiguous() else w.contiguous() for _, w in named],
+                               stream=stream) / 6.0
+        made = [(torch.empty(c, dtype=torch.uint8, device=w.device),
+                 torch.empty(s, dtype=torch.uint8, device=w.device))
+                for (c, s), (_, w) in zip(shapes, named)]
+    recs, out = [], []
+    for i, ((name, w), (codes, scales)) in enumerate(zip(named, made)):
+        t = None if ts is None else ts[i:i + 1]
+        recs.append(_FP4_DESC.pack(*_fp4_record(w, name, format, codes.data_ptr(),
+                                                scales.data_ptr(), t)))
+        out += [(name, codes), (name + "_scale", scales)]
+        if t is not None:
+            out.append((name + "_scale_2", t))
+    check(lib().fp8bq_fp4_quantize_batched(b"".join(recs), len(recs), _stream(stream)),
+          "quant_weights_fp4")
+    return out
+
+
+def _fp4_operand(codes, scales, tensor_scale, format: str, block: int, what: str):
+    """The fields of an ``fp8bq_fp4_operand``, and (batch or 0, rows, code bytes a row)."""
+    import torch
+    _check_cuda(codes, what)
+    _check_cuda(scales, f"{what}'s scales")
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise TypeError(f"{what}: codes and scales must be uint8")
+    dim = codes.dim()
+    if dim not in (2, 3) or scales.dim() != dim + 2:
+        raise ValueError(f"{what}: expected codes [(E,) M, K / 2] and scales "
+                         "[(E,) M tiles, K tiles, 32, 16]")
+    shape, st = codes.shape, codes.stride()
+    rows, kb = shape[-2], shape[-1]
+    want = (*shape[:-2], -(-rows // 128), -(-2 * kb // (4 * block)), 32, 16)
+    if kb % 16 or tuple(scales.shape) != want:
+        raise ValueError(f"{what}: codes {tuple(shape)} go with {format} scales {want}, "
+                         f"got {tuple(scales.shape)}")
+    ss = scales.stride()
+    if (kb > 1 and st[-1] != 1) or (rows > 1 and st[-2] != kb):
+        raise ValueError(f"{what}: the codes' rows must be contiguous")
+    if ss[-1] != 1 or ss[-2] != 16 or (want[-3] > 1 and ss[-3] != 512) or \
+            (want[-4] > 1 and ss[-4] != 512 * want[-3]):
+        raise ValueError(f"{what}: the scale tiles must be contiguous")
+    E = shape[0] if dim == 3 else 0
+    t, ts = _fp4_tensor_scale(tensor_scale, max(E, 1), format, f"{what}'s tensor scale")
+    return ((codes.data_ptr(), scales.data_ptr(), t, st[0] if E else 0, ss[0] if E else 0, ts),
+            (E, rows, kb))
+
+
+def dequantize_fp4_blockwise(codes, scales, format="mxfp4", columns=None, tensor_scale=None,
+                             out_dtype=None, stream=None):
+    """Reverse map of ``scaled_fp4_blockwise``: the values as bf16 (default) or
+    fp32, [(E,) M, columns] (default: every column the codes have room for)."""
+    import torch
+    fmt, block = _fp4_format(format)
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+    K = 2 * codes.shape[-1] if columns is None else int(columns)
+    if K < 0 or -(-K // 32) * 16 != codes.shape[-1]:
+        raise ValueError(f"codes of {codes.shape[-1]} bytes a row do not hold {K} columns")
+    if K == 0:
+        return torch.empty((*codes.shape[:-1], 0), dtype=out_dtype, device=codes.device)
+    (c, s, t, cbs, sbs, ts), (E, M, kb) = _fp4_operand(codes, scales, tensor_scale, format, block,
+                                                       "codes")
+    if E > 1 and (cbs != M * kb or sbs != scales[0].numel()):
+        raise ValueError("a stack's codes and scales must be contiguous")
+    with _on_stream(stream):
+        out = torch.empty((*codes.shape[:-1], K), dtype=out_dtype, device=codes.device)
+    check(lib().fp8bq_fp4_dequantize(c, s, E if codes.dim() == 3 else 1, M, K, fmt, t, ts,
+                                     out.data_ptr(),
+                                     FP8BQ_BF16 if out_dtype == torch.bfloat16 else FP8BQ_F32, K,
+                                     M * K, _stream(stream)), "dequantize_fp4_blockwise")
+    return out
+
+
+_FP4_NONE = (0, 0, 0, 0, 0, 0)
+
+
+def _fp4_product(entry, a, weights, format, out_dtype, rows, out, stream, what):
+    import torch
+    fmt, block = _fp4_format(format)
+    fa, (E, M, kb) = _fp4_operand(*a, format, block, "a")
+    fields = list(fa)
+    N = -1
+    for name, w in weights:
+        fw, (Ew, n, kw) = _fp4_operand(*w, format, block, name)
+        if Ew != E or kw != kb or N not in (-1, n) or w[0].dim() != a[0].dim():
+            raise ValueError(f"{name}: shape {tuple(w[0].shape)} does not match "
+                             f"a {tuple(a[0].shape)} or the other weight")
+        N = n
+        fields += fw
+    if len(weights) == 1:
+        fields += _FP4_NONE
+    shape = (E, M, N) if a[0].dim() == 3 else (M, N)
+    if rows is not None:
+        _check_cuda(rows, "rows")
+        if a[0].dim() != 3 or rows.dtype != torch.int32 or rows.shape != (E,) or \
+                not rows.is_contiguous():
+            raise ValueError("rows must be int32, contiguous, one value for each matrix of a stack")
+    if out is None:
+        out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+        if out_dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
+        with _on_stream(stream):
+            make = torch.empty if rows is None else torch.zeros
+            out = make(shape, dtype=out_dtype, device=a[0].device)
+    else:
+        _check_cuda(out, "out")
+        if out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out must be {shape} {out_dtype or ''}, got {tuple(out.shape)} "
+                             f"{out.dtype}")
+        _dtype_code(out)
+        if N > 1 and out.stride(-1) != 1:
+            raise ValueError("the last dimension of out must have unit stride")
+    st = out.stride()
+    fields += (out.data_ptr(), 0 if rows is None else rows.data_ptr(), M, N, 2 * kb,
+               E if len(shape) == 3 else 1, max(st[-2] if M > 1 else N, N),
+               st[0] if len(shape) == 3 else 0, fmt,
+               FP8BQ_BF16 if out.dtype == torch.bfloat16 else FP8BQ_F32)
+    check(entry(_FP4_MATMUL_DESC.pack(*fields), _stream(stream)), what)
+    return out
+
+
+def matmul_fp4(a, a_scales, b, b_scales, format="mxfp4", a_tensor_scale=None, b_tensor_scale=None,
+               out_dtype=None, rows=None, out=None, stream=None):
+    """The product a b^T of 4-bit matrices, as ``scaled_fp4_blockwise`` makes
+    them: a [(E,) M, K] (tokens), b [(E,) N, K] (a weight), both of one format.
+    Returns [(E,) M, N] in bf16 (default) or fp32, or ``out`` filled.
+
+    ``rows`` (int32 CUDA tensor, one value for each matrix of a stack): only the
+    first rows[e] rows of a[e] are used, and the rows of out[e] behind them are
+    left as they were (zeros in an output made here).
+
+    The codes carry no gradient: they are what an inference engine holds.
+    """
+    return _fp4_product(lib().fp8bq_fp4_matmul, (a, a_scales, a_tensor_scale),
+                        (("b", (b, b_scales, b_tensor_scale)),), format, out_dtype, rows, out,
+                        stream, "matmul_fp4")
+
+
+def gated_matmul_fp4(a, a_scales, gate, gate_scales, up, up_scales, format="mxfp4",
+                     a_tensor_scale=None, gate_tensor_scale=None, up_tensor_scale=None,
+                     out_dtype=None, rows=None, out=None, stream=None):
+    """silu(a gate^T) * (a up^T), the gated half of a feed-forward block, in one
+    kernel; operands and arguments as in ``matmul_fp4``.  The halves of a fused
+    [(E,) 2F, K] weight may be views of it where F is a multiple of 128
+    (codes[..., :F, :], scales[..., :F // 128, :, :, :], and the rest)."""
+    return _fp4_product(lib().fp8bq_fp4_gated_matmul, (a, a_scales, a_tensor_scale),
+                        (("gate", (gate, gate_scales, gate_tensor_scale)),
+                         ("up", (up, up_scales, up_tensor_scale))), format, out_dtype, rows, out,
+                        stream, "gated_matmul_fp4")

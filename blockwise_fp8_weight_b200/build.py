@@ -20,15 +20,18 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("fp8bq_api.cu", "fp8bq_kernels.cu", "fp8bq_tma.cu",
-                                                   "fp8bq_dequant.cu", "fp8bq_scale.cu")]
+                                                   "fp8bq_dequant.cu", "fp8bq_scale.cu",
+                                                   "fp8bq_fp4_api.cu", "fp8bq_fp4_quant.cu",
+                                                   "fp8bq_fp4_mm.cu")]
 HEADERS = [os.path.join(CSRC, f) for f in ("fp8bq_internal.h", "fp8bq_device.cuh",
-                                                   "fp8bq_tile.cuh")] + [
+                                                   "fp8bq_tile.cuh", "fp8bq_fp4.h",
+                                                   "fp8bq_fp4_device.cuh")] + [
     os.path.join(ROOT, "include", "fp8bq.h")]
 LIB = os.path.join(PKG, "libfp8bq.so")
 LIB_CHECKED = os.path.join(PKG, "libfp8bq_checked.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
-FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-shared", "-Xcompiler", "-fPIC,-fvisibility=hidden",
+FLAGS = ["-O3", "-std=c++17", "--threads", "0", "-lineinfo", "-shared", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          "-cudart", "static", "--expt-relaxed-constexpr",
          # IEEE division/sqrt and no flush-to-zero (nvcc's defaults, stated explicitly)
          "-prec-div=true", "-prec-sqrt=true", "-ftz=false", "-fmad=true"]

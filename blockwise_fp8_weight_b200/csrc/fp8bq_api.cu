@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "../../include/fp8bq.h"
+#include "fp8bq_fp4.h"
 #include "fp8bq_internal.h"
 
 using namespace fp8bq;
@@ -912,7 +913,8 @@ fp8bq_status run_tensor_scale(const fp8bq_scale_desc *t, int n, float *scale_out
 // zeros without any CUDA call in a default build).
 cudaError_t bounds_records(uint64_t *count, uint64_t *first, bool clear) {
     cudaError_t (*const fns[])(uint64_t *, uint64_t *, bool) = {
-        bounds_record_kernels, bounds_record_tma, bounds_record_dequant, bounds_record_scale};
+        bounds_record_kernels,   bounds_record_tma, bounds_record_dequant, bounds_record_scale,
+        bounds_record_fp4_quant, bounds_record_fp4_mm};
     *count = 0;
     *first = 0;
     for (auto fn : fns) {
@@ -928,6 +930,13 @@ cudaError_t bounds_records(uint64_t *count, uint64_t *first, bool clear) {
 }  // namespace
 
 bool fp8bq::pdl_enabled() { return g_pdl.load(std::memory_order_relaxed) != 0; }
+
+// What the 4-bit entry points (fp8bq_fp4_api.cu) share with these.
+fp8bq_status fp8bq::device_status() { return check_device(); }
+uint64_t fp8bq::wait_limit() { return g_wait_limit_ns.load(); }
+uint32_t fp8bq::inject_flags() { return g_inject.load(); }
+uint64_t fp8bq::checked_extent(uint64_t bytes) { return checked_out_extent(bytes); }
+PFN_cuTensorMapEncodeTiled_v12000 fp8bq::tensor_map_encoder() { return encode_fn(); }
 
 extern "C" {
 
@@ -1013,11 +1022,13 @@ fp8bq_status fp8bq_sync_status(cudaStream_t stream) {
         cudaGetLastError();
         return FP8BQ_ERR_DEVICE;
     }
-    uint32_t w = 0;
-    if (read_and_clear_error_word(&w) != cudaSuccess) {
+    uint32_t w = 0, w4 = 0;
+    if (read_and_clear_error_word(&w) != cudaSuccess ||
+        read_and_clear_fp4_error_word(&w4) != cudaSuccess) {
         cudaGetLastError();
         return FP8BQ_ERR_DEVICE;
     }
+    w |= w4;
     if (w & 2u) return FP8BQ_ERR_DEVICE_UNSAFE;
     if (w) return FP8BQ_ERR_DEVICE_TIMEOUT;
     uint64_t count = 0, first = 0;

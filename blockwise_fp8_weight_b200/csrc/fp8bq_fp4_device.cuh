@@ -1,0 +1,150 @@
+// fp8bq_fp4_device.cuh -- the sm_100a instructions of the 4-bit products:
+// tensor memory, block-scaled tcgen05.mma, their completion barriers, and
+// thread-block cluster access.
+#pragma once
+
+#include "fp8bq_device.cuh"
+#include "fp8bq_fp4.h"
+
+namespace fp8bq {
+namespace dev {
+
+// ---------------------------------------------------------------- tensor memory
+
+// One warp; CG CTAs of a pair allocate together (each has a warp make the
+// call).  The base address lands in *dst (shared memory).
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t cols) {
+    if constexpr (CG == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(dst)), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_addr(dst)), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_dealloc(uint32_t base, uint32_t cols) {
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
+}
+
+__device__ __forceinline__ void tc_fence_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// 16 columns of this warp's 32 lanes (lane i of the warp gets lane i of its
+// quarter), and the wait for them.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
+          "=r"(v[14]), "=r"(v[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld_wait() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- shared-memory operands
+
+// Descriptor of a K-major operand of 128-byte rows in the 128-byte swizzle
+// (groups of eight rows 1024 bytes apart), starting at a 1024-byte boundary;
+// 32 bytes (64 codes) along K are two units of its address field.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+// Descriptor of a 512-byte scale tile: 32 rows of 16 bytes, no swizzle,
+// groups of eight rows 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3ffff) >> 4) | (8ull << 16) | (8ull << 32) | (1ull << 46);
+}
+
+// A scale tile into four tensor-memory columns (row r: lane r % 32 of every
+// quarter, column r / 32, its four blocks in the column's four bytes).
+template <int CG>
+__device__ __forceinline__ void scales_to_tmem(uint32_t dst, uint64_t desc) {
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(dst), "l"(desc));
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(dst), "l"(desc));
+}
+
+// ---------------------------------------------------------------- block-scaled MMA
+
+// Instruction word: e2m1 operands, fp32 sums, both K-major, tile m x n, e8m0
+// or e4m3 scales; byte `id` of a scale column begins the instruction's.
+__host__ __device__ constexpr uint32_t mma_word(int format, int m, int n) {
+    return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) |
+           ((format == FP8BQ_MXFP4 ? 1u : 0u) << 23) | ((uint32_t)(m >> 7) << 27);
+}
+__device__ __forceinline__ uint32_t mma_word_id(uint32_t word, uint32_t id) {
+    return word | (id << 4) | (id << 29);
+}
+
+template <int FMT, int CG>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t word,
+                                        uint32_t sa, uint32_t sb, bool add) {
+#define FP4_MMA(CGS, VEC)                                                                     \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"                             \
+                 "tcgen05.mma.cta_group::" CGS ".kind::mxf4nvf4.block_scale.scale_vec::" VEC  \
+                 " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(word), \
+                 "r"(sa), "r"(sb), "r"((uint32_t)add)                                          \
+                 : "memory")
+    if constexpr (CG == 1 && FMT == FP8BQ_MXFP4) FP4_MMA("1", "2X");
+    else if constexpr (CG == 1) FP4_MMA("1", "4X");
+    else if constexpr (FMT == FP8BQ_MXFP4) FP4_MMA("2", "2X");
+    else FP4_MMA("2", "4X");
+#undef FP4_MMA
+}
+
+// Arrive on `bar` once everything this thread has issued to the tensor cores
+// is done; CG == 2: on the barrier at this place in both CTAs of the pair.
+template <int CG>
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                         smem_addr(bar)) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+                     ".multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)), "h"((uint16_t)3)
+                     : "memory");
+}
+
+// ---------------------------------------------------------------- clusters
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 peer_ld4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+}  // namespace dev
+}  // namespace fp8bq

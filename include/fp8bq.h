@@ -233,6 +233,124 @@ typedef struct fp8bq_scale_desc {
 FP8BQ_API fp8bq_status fp8bq_tensor_scale(const fp8bq_scale_desc *desc_table, int n_tensors,
                                           float *scale_out, cudaStream_t stream);
 
+/*
+ * ---------------------------------------------------------------- 4-bit operators
+ *
+ * Microscaled 4-bit floating point: e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives) with one scale for each run of values along a row.
+ *
+ *   FP8BQ_MXFP4  32 values a scale, a power of two (e8m0, OCP MX v1.0):
+ *       S     = clamp(floor(log2 a) - 2, -127, 127), a = max|x| of the block
+ *               (S = -127 for a = 0);  scale byte S + 127
+ *       code  = e2m1(x * 2^-S)
+ *       value = e2m1 value * 2^S
+ *   FP8BQ_NVFP4  16 values a scale (e4m3), and one fp32 scale t of the tensor:
+ *       s     = e4m3(min((a / 6) / t, 448))     (IEEE fp32 divisions)
+ *       d     = s * t;  r = 1 / d, 0 if d = 0   (each rounded to fp32)
+ *       code  = e2m1(x * r)                     (the product rounded to fp32)
+ *       value = e2m1 value * s * t
+ *       t > 0; NULL means 1.  max|X| / (6 * 448) makes the largest block's s
+ *       448: fp8bq_tensor_scale's result divided by 6.
+ *
+ * e2m1() rounds to nearest, ties to even, takes magnitudes beyond 6 to 6 and
+ * keeps the sign of a result that rounds to zero.  A block that holds an
+ * infinity or a NaN gets the NaN scale (0xFF, 0x7F) and zero codes, so its
+ * values are NaN.
+ *
+ * Layout of an [M, K] matrix (a stack of them: one after the other, or at the
+ * stated strides where an operand has them):
+ *   codes   M rows of 16 * ceil(K / 32) bytes, two codes a byte, the even
+ *           column in the low half; codes of columns >= K are 0.
+ *   scales  [ceil(M / 128), ceil(K / (4 B))] tiles of 512 bytes, B the block
+ *           length (32, 16): the scale of row r and block j is byte
+ *           (r % 32) * 16 + (r % 128) / 32 * 4 + j % 4 of tile (r / 128, j / 4);
+ *           bytes beyond the matrix are 0.
+ * Both 16-byte aligned.  M and K at most 2^31 - 256.
+ */
+typedef enum fp8bq_fp4_format { FP8BQ_MXFP4 = 0, FP8BQ_NVFP4 = 1 } fp8bq_fp4_format;
+
+/* One stack of a grouped 4-bit quantisation; codes and scales contiguous. */
+typedef struct fp8bq_fp4_desc {
+    const void *x;               /* device, matrix b at x + b * x_batch_stride, rows ld apart */
+    uint8_t *codes, *scales;     /* device, written (every byte of both) */
+    const float *tensor_scale;   /* device or NULL; NULL for MXFP4 */
+    int64_t M, K, ld, batch;
+    int64_t x_batch_stride;      /* elements; ignored for batch == 1 */
+    int64_t tensor_scale_stride; /* floats from one matrix's scale to the next's; 0: shared */
+    int32_t dtype_in, format;    /* fp8bq_dtype, fp8bq_fp4_format */
+} fp8bq_fp4_desc;
+
+/*
+ * Quantise to 4 bits: one matrix, or a list of stacks in one launch for each
+ * format, input type and alignment.  Checks, status codes, overlap rules and
+ * stream semantics are those of fp8bq_quantize(_batched); FP8BQ_ERR_ARG for an
+ * unknown format or a tensor scale given with FP8BQ_MXFP4.
+ */
+FP8BQ_API fp8bq_status fp8bq_fp4_quantize(const void *x, fp8bq_dtype dtype_in, int64_t M,
+                                          int64_t K, int64_t ld, fp8bq_fp4_format format,
+                                          const float *tensor_scale, uint8_t *codes,
+                                          uint8_t *scales, cudaStream_t stream);
+FP8BQ_API fp8bq_status fp8bq_fp4_quantize_batched(const fp8bq_fp4_desc *desc_table, int n_tensors,
+                                                  cudaStream_t stream);
+
+/*
+ * The values of a stack of 4-bit matrices as bf16 or fp32: matrix b at out +
+ * b * out_batch_stride, rows ld_out >= K elements apart.  e2m1 * scale is
+ * exact in fp32; the product with t and the output's type each round once.
+ */
+FP8BQ_API fp8bq_status fp8bq_fp4_dequantize(const uint8_t *codes, const uint8_t *scales,
+                                            int64_t batch, int64_t M, int64_t K,
+                                            fp8bq_fp4_format format, const float *tensor_scale,
+                                            int64_t tensor_scale_stride, void *out,
+                                            fp8bq_dtype dtype_out, int64_t ld_out,
+                                            int64_t out_batch_stride, cudaStream_t stream);
+
+/* A stack of 4-bit matrices that a product reads.  Strides are ignored for
+ * batch == 1 and may be those of rows [n0, n1) of larger matrices where n0 is
+ * a multiple of 128 (codes of row n0, scales of its tile row). */
+typedef struct fp8bq_fp4_operand {
+    const uint8_t *codes, *scales; /* device */
+    const float *tensor_scale;     /* device or NULL (1); NULL for MXFP4 */
+    int64_t codes_batch_stride;    /* bytes, a multiple of 16; 0: one matrix for all */
+    int64_t scales_batch_stride;   /* bytes, a multiple of 16; 0: one matrix for all */
+    int64_t tensor_scale_stride;   /* floats; 0: shared */
+} fp8bq_fp4_operand;
+
+/*
+ * Products of 4-bit matrices, all of one format, for each matrix e of a stack:
+ *
+ *   fp8bq_fp4_matmul        out[e] = a[e] b[e]^T
+ *   fp8bq_fp4_gated_matmul  out[e] = silu(a[e] b[e]^T) * (a[e] up[e]^T),
+ *                           silu(v) = v / (1 + exp(-v)); b is the gate
+ *
+ * a is [M, K] (tokens), b and up are [N, K] (weights, one row for each output
+ * column), out is [M, N] in bf16 or fp32.  Products and sums are those of the
+ * tensor cores, held in fp32; tensor scales, the activation and the gate's
+ * product are fp32; the result is rounded once.  A K range may be summed in
+ * parts, always the same ones in the same order for the same call: results
+ * repeat bit for bit.
+ *
+ *   rows  device, batch int32, or NULL: only the first rows[e] rows of a[e]
+ *         are used (values beyond M count as M, below 0 as 0); the rows of
+ *         out[e] behind them are left as they were.  Read on the stream.
+ *
+ * K >= 1 (FP8BQ_ERR_SHAPE otherwise: an empty sum is refused).  Empty M, N or
+ * batch: nothing is done.  batch and ceil(M / 128) at most 65535.  out must
+ * overlap no input, and its matrices not each other.
+ */
+typedef struct fp8bq_fp4_matmul_desc {
+    fp8bq_fp4_operand a, b, up; /* up: fp8bq_fp4_gated_matmul only */
+    void *out;                  /* device, matrix e at out + e * out_batch_stride elements */
+    const int32_t *rows;        /* device or NULL */
+    int64_t M, N, K, batch;
+    int64_t ld_out, out_batch_stride; /* elements; ld_out >= N */
+    int32_t format, dtype_out;        /* fp8bq_fp4_format, fp8bq_dtype */
+} fp8bq_fp4_matmul_desc;
+
+FP8BQ_API fp8bq_status fp8bq_fp4_matmul(const fp8bq_fp4_matmul_desc *desc, cudaStream_t stream);
+FP8BQ_API fp8bq_status fp8bq_fp4_gated_matmul(const fp8bq_fp4_matmul_desc *desc,
+                                              cudaStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 FP8BQ_API const char *fp8bq_status_string(fp8bq_status status);
 
