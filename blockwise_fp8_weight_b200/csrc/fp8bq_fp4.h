@@ -87,7 +87,7 @@ struct Fp4MmParams {
     int32_t stages_k;  // ceil(K / 256)
     int32_t mma_k;     // ceil(K / 64)
     int32_t split;     // CTAs that share a tile's K range (a cluster)
-    int32_t store_vec; // elements of the widest aligned store (8, 4, 2 or 1)
+    int32_t store_align; // bytes (32, 16, 8 or the element's) that every output row is aligned to
     uint32_t moves;    // bit i: operand map i steps with the stack (x, xs, w[0], ws[0], w[1], ws[1])
     uint32_t inject;
 #if FP8BQ_CHECKED
@@ -99,6 +99,9 @@ struct Fp4MmParams {
 cudaError_t launch_fp4_mm_narrow(const Fp4MmParams &p, int format, bool gated, bool out_bf16,
                                  int tokens, cudaStream_t st);
 int fp4_narrow_tokens(int64_t M, bool gated);
+// Tiles of 256 tokens by 256 outputs (gated: 128) on pairs of SMs.
+cudaError_t launch_fp4_mm_wide(const Fp4MmParams &p, int format, bool gated, bool out_bf16,
+                               cudaStream_t st);
 
 cudaError_t read_and_clear_fp4_error_word(uint32_t *out);
 cudaError_t bounds_record_fp4_quant(uint64_t *count, uint64_t *first, bool clear);

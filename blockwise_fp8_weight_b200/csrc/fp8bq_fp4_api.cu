@@ -305,10 +305,11 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     const fp8bq_status sd = device_status();
     if (sd != FP8BQ_OK) return sd;
 
+    const bool wide = D.M > 256;
     const int tokens = fp4_narrow_tokens(D.M, gated);
     Fp4MmParams p;
     std::memset(&p, 0, sizeof p);
-    bool ok = map_codes(mats[0], D, tokens, &p.x) && map_scales(mats[0], D, &p.xs);
+    bool ok = map_codes(mats[0], D, wide ? 128 : tokens, &p.x) && map_scales(mats[0], D, &p.xs);
     for (int i = 1; ok && i < n; ++i)
         ok = map_codes(mats[i], D, 128, &p.w[i - 1]) && map_scales(mats[i], D, &p.ws[i - 1]);
     if (!ok) return FP8BQ_ERR_DEVICE;
@@ -330,10 +331,10 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     p.stages_k = (int32_t)((kb + 127) / 128);
     p.mma_k = (int32_t)((kb + 31) / 32);
     p.split = 1;
-    p.store_vec = 1;
-    for (int v : {8, 4})
-        if (p.store_vec == 1 && (uintptr_t)D.out % (v * es) == 0 && D.ld_out % v == 0 && obs % v == 0)
-            p.store_vec = v;
+    p.store_align = es;
+    for (int a : {8, 16, 32})
+        if ((uintptr_t)D.out % a == 0 && D.ld_out * es % a == 0 && obs * es % a == 0)
+            p.store_align = a;
     for (int i = 0; i < n; ++i)  // a stack stride of 0: one matrix for the whole stack
         p.moves |= (mats[i].cbs ? 1u : 0u) << (2 * i) | (mats[i].sbs ? 2u : 0u) << (2 * i);
     p.inject = inject_flags();
@@ -343,8 +344,9 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     p.xt_bytes = (uint64_t)mats[0].t_bytes;
     for (int i = 1; i < n; ++i) p.wt_bytes[i - 1] = (uint64_t)mats[i].t_bytes;
 #endif
-    if (launch_fp4_mm_narrow(p, D.format, gated, D.dtype_out == FP8BQ_BF16, tokens, stream) !=
-        cudaSuccess) {
+    const bool bf16 = D.dtype_out == FP8BQ_BF16;
+    if ((wide ? launch_fp4_mm_wide(p, D.format, gated, bf16, stream)
+              : launch_fp4_mm_narrow(p, D.format, gated, bf16, tokens, stream)) != cudaSuccess) {
         cudaGetLastError();
         return FP8BQ_ERR_DEVICE;
     }

@@ -53,7 +53,7 @@ __device__ __forceinline__ void store4(const Fp4MmParams &p, int64_t e, int64_t 
                                        const float (&v)[4]) {
     constexpr int ES = BF16 ? 2 : 4;
     char *dst = (char *)p.out + (e * p.obs + m * p.ldo + n) * ES;
-    if (p.store_vec >= 4 && n + 4 <= p.N) {
+    if (p.store_align >= 4 * ES && n + 4 <= p.N) {
         if (!FP8BQ_IN(MM_SPAN(p.out, p.out_bytes), dst, 4 * ES)) return;
         if constexpr (BF16) *(uint2 *)dst = make_uint2(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]));
         else *(float4 *)dst = make_float4(v[0], v[1], v[2], v[3]);
@@ -288,6 +288,290 @@ __global__ void __launch_bounds__(128) k_fp4_narrow(const __grid_constant__ Fp4M
     if (warp == 1) dev::tmem_dealloc<1>(tmem, S::kCols);
 }
 
+// ============================================================== many tokens
+//
+// A pair of SMs (cta_group::2) computes 256 tokens by 256 outputs: each CTA
+// holds the codes of its 128 tokens and of half of the weight's 256 rows, and
+// the tensor cores of both read both halves, so a stage of 256 columns of K
+// costs each SM 32 KB of codes for 128 x 256 outputs.  Gated: 128 outputs, the
+// first half of the 256 weight rows from the gate, the other from `up`, so the
+// two sums of an output lie 128 columns apart in the same tensor-memory lane.
+//
+// Persistent: a pair walks over tiles.  In each CTA warp 0 loads (one lane),
+// warps 4-11 store; warp 1 of the first CTA issues the products of both.  The
+// sums of successive tiles alternate between columns [0, 256) and [160, 416),
+// so the next tile is multiplied while this one is stored; the 96 columns that
+// both use are stored first, and the next tile waits for those alone.  The
+// scales' two buffers take the last 96 columns.
+template <int FMT>
+struct Wide {
+    static constexpr int KT = 256 / (4 * fp4_block(FMT));
+    static constexpr int SF = KT * kFp4TileBytes;
+    static constexpr int kCodes = 128 * 128;                   // 128 rows
+    static constexpr int kStage = 2 * kCodes + 3 * SF;         // tokens, weight, their scales
+    static constexpr int kSmem = 231424;                       // an SM to itself
+    static constexpr int kStages = (kSmem - 1024) / kStage;
+    static constexpr int kOther = 160;                         // columns of the odd tiles' sums
+    static constexpr int kScales = 416;
+    static constexpr int kSfCols = 12 * KT;
+    static constexpr int kThreads = 384;
+    static_assert(2 * kSfCols <= 512 - kScales, "tensor memory");
+};
+
+// 32 consecutive outputs of a row, from column n; `align` bytes.
+template <bool BF16>
+__device__ __forceinline__ void store32(const Fp4MmParams &p, int64_t e, int64_t m, int n,
+                                        const float (&v)[32]) {
+    constexpr int ES = BF16 ? 2 : 4, PER = 32 / ES;            // outputs in 32 bytes
+    char *dst = (char *)p.out + (e * p.obs + m * p.ldo + n) * ES;
+#pragma unroll
+    for (int c = 0; c < 32; c += PER, dst += 32) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            w[j] = BF16 ? bf16x2(v[(c + 2 * j) & 31], v[(c + 2 * j + 1) & 31])
+                        : __float_as_uint(v[(c + j) & 31]);
+        if (n + c + PER <= p.N && p.store_align >= 16) {
+            if (!FP8BQ_IN(MM_SPAN(p.out, p.out_bytes), dst, 32)) continue;
+            if (p.store_align >= 32) {
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
+                             "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+                             "r"(w[6]), "r"(w[7])
+                             : "memory");
+            } else {
+                *(uint4 *)dst = make_uint4(w[0], w[1], w[2], w[3]);
+                *(uint4 *)(dst + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (n + c + j < p.N &&
+                    FP8BQ_IN(MM_SPAN(p.out, p.out_bytes), dst + j * ES, ES)) {
+                    if constexpr (BF16)
+                        *(uint16_t *)(dst + j * 2) = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+                    else
+                        *(uint32_t *)(dst + j * 4) = w[j & 7];
+                }
+        }
+    }
+}
+
+// The tiles of a pair: first rows, first outputs and matrix of the stack, in
+// the same order for every role; tiles without valid rows are passed over.
+struct WideWalk {
+    const Fp4MmParams &p;
+    int64_t t, step, total;
+    int mt, nt, width;
+    int m0, n0, e, valid;
+    __device__ __forceinline__ WideWalk(const Fp4MmParams &q, int width_)
+        : p(q), t((int64_t)(blockIdx.x >> 1) - (gridDim.x >> 1)), step(gridDim.x >> 1), width(width_) {
+        mt = (p.M + 255) / 256;
+        nt = (p.N + width - 1) / width;
+        total = (int64_t)mt * nt * p.batch;
+    }
+    __device__ __forceinline__ bool next() {
+        while ((t += step) < total) {
+            const int64_t r = t / mt;
+            e = (int)(r / nt);
+            m0 = (int)(t - r * mt) * 256;
+            n0 = (int)(r - (int64_t)e * nt) * width;
+            valid = valid_rows(p, e);
+            if (m0 < valid) return true;
+        }
+        return false;
+    }
+};
+
+template <int FMT, bool GATED, bool BF16>
+__global__ void __launch_bounds__(384) k_fp4_wide(const __grid_constant__ Fp4MmParams p) {
+    using S = Wide<FMT>;
+    extern __shared__ uint8_t raw[];
+    // full, drained: the first CTA's count; empty, sums: each CTA its own
+    __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], sums, drained, done;
+    __shared__ uint32_t tmem_at;
+    __shared__ volatile int abort_flag;
+    uint8_t *ring = raw + ((1024u - (dev::smem_addr(raw) & 1023u)) & 1023u);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = dev::cluster_rank();
+    constexpr int kWidth = GATED ? 128 : 256;
+    if (tid == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            dev::mbar_init(&full[s], 1);
+            dev::mbar_init(&empty[s], 1);
+        }
+        dev::mbar_init(&sums, 1);
+        dev::mbar_init(&drained, 16);
+        dev::mbar_init(&done, 1);
+        abort_flag = 0;
+        dev::fence_mbar_init();
+        dev::prefetch_tensormap(&p.w[0]);
+        dev::prefetch_tensormap(&p.x);
+    }
+    if (warp == 1) dev::tmem_alloc<2>(&tmem_at, 512);
+    dev::tc_fence_before();
+    dev::cluster_sync();  // the pair's barriers and tensor memory are there
+    dev::tc_fence_after();
+    dev::pdl_launch_dependents();
+    dev::pdl_wait();
+    const uint32_t tmem = tmem_at;
+    auto gave_up = [&] {
+        if (!abort_flag) {
+            atomicOr(&g_fp4_error_word, 1u);
+            abort_flag = 1;
+        }
+    };
+
+    WideWalk w(p, kWidth);
+    if (warp == 0 && lane == 0) {
+        auto at = [&](int map) { return (p.moves >> map) & 1u ? w.e : 0; };
+        bool dropped = false, ok = true;
+        int i = 0;  // stages loaded
+        while (ok && w.next()) {
+            for (int k = 0; k < p.stages_k; ++k, ++i) {
+                const int st = i % S::kStages, round = i / S::kStages;
+                if (round > 0 && !dev::mbar_wait_bounded(&empty[st], (round - 1) & 1,
+                                                         p.wait_limit_ns, &abort_flag)) {
+                    gave_up();
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = dev::peer_addr(dev::smem_addr(&full[st]), 0);
+                if (rank == 0) dev::mbar_arrive_expect_tx(&full[st], 2 * S::kStage);
+                if ((p.inject & FP8BQ_INJECT_DROP_FIRST_LOAD) && i == 0 && blockIdx.x == 0) {
+                    dropped = true;
+                    continue;
+                }
+                uint8_t *b = ring + st * S::kStage;
+                const int wn = GATED ? w.n0 : w.n0 + (int)rank * 128;
+                const int wi = GATED ? (int)rank : 0;
+                dev::tma_load_3d_pair(b, &p.x, bar, k * 128, w.m0 + (int)rank * 128, at(0));
+                dev::tma_load_3d_pair(b + S::kCodes, &p.w[wi], bar, k * 128, wn, at(2 + 2 * wi));
+                b += 2 * S::kCodes;
+                dev::tma_load_3d_pair(b, &p.xs, bar, k * (S::SF / 8), w.m0 / 128 + (int)rank, at(1));
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    dev::tma_load_3d_pair(b + (1 + h) * S::SF, &p.ws[GATED ? h : 0], bar,
+                                          k * (S::SF / 8), w.n0 / 128 + (GATED ? 0 : h),
+                                          at(3 + (GATED ? 2 * h : 0)));
+            }
+        }
+        // Every copy of both CTAs has landed (a dropped stage's others had the
+        // whole wait that ran out for it).
+        for (int st = 0; rank == 0 && st < S::kStages && st < i; ++st) {
+            const int fills = (i - st + S::kStages - 1) / S::kStages;
+            if (dropped && st == 0 && fills == 1) continue;
+            if (!dev::mbar_wait_bounded(&full[st], (fills - 1) & 1, kDrainNs, nullptr))
+                atomicOr(&g_fp4_error_word, 2u);
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        constexpr uint32_t word = dev::mma_word(FMT, 256, 256);
+        bool ok = true;
+        int i = 0, n = 0;  // stages, tiles
+        for (; ok && w.next(); ++n) {
+            if (n > 0 && !dev::mbar_wait_bounded(&drained, (n - 1) & 1, p.wait_limit_ns,
+                                                 &abort_flag)) {
+                gave_up();
+                break;
+            }
+            dev::tc_fence_after();
+            const uint32_t d = tmem + (n & 1) * S::kOther;
+            for (int k = 0; k < p.stages_k; ++k, ++i) {
+                const int st = i % S::kStages;
+                if (!dev::mbar_wait_bounded(&full[st], (i / S::kStages) & 1, p.wait_limit_ns,
+                                            &abort_flag)) {
+                    gave_up();
+                    ok = false;
+                    break;
+                }
+                dev::tc_fence_after();
+                const uint32_t at = dev::smem_addr(ring + st * S::kStage);
+                const uint32_t sf = at + 2 * S::kCodes;
+                const uint32_t sx = tmem + S::kScales + (i & 1) * S::kSfCols;
+                const uint32_t sw = sx + 4 * S::KT;
+#pragma unroll
+                for (int t = 0; t < S::KT; ++t) {
+                    dev::scales_to_tmem<2>(sx + 4 * t, dev::scale_desc(sf + t * kFp4TileBytes));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        dev::scales_to_tmem<2>(
+                            sw + 8 * t + 4 * h,
+                            dev::scale_desc(sf + (1 + h) * S::SF + t * kFp4TileBytes));
+                }
+                const uint64_t xd = dev::operand_desc(at), wd = dev::operand_desc(at + S::kCodes);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (4 * k + j >= p.mma_k) break;
+                    const int t = j * S::KT / 4;
+                    dev::mma_fp4<FMT, 2>(
+                        d, xd + 2 * j, wd + 2 * j,
+                        dev::mma_word_id(word, FMT == FP8BQ_MXFP4 ? 2 * (j & 1) : 0), sx + 4 * t,
+                        sw + 8 * t, k + j > 0);
+                }
+                dev::mma_commit<2>(&empty[st]);
+            }
+            dev::mma_commit<2>(&sums);
+        }
+        dev::mma_commit_pair_here(&done);
+        if (!dev::mbar_wait_bounded(&done, 0, kDrainNs, nullptr)) atomicOr(&g_fp4_error_word, 2u);
+    } else if (warp >= 4) {
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t drained_bar = dev::peer_addr(dev::smem_addr(&drained), 0);
+        for (int n = 0; w.next(); ++n) {
+            const bool here =
+                dev::mbar_wait_bounded(&sums, n & 1, 2 * p.wait_limit_ns, &abort_flag);
+            if (!__all_sync(0xffffffffu, here)) {
+                if (lane == 0) gave_up();
+                break;
+            }
+            dev::tc_fence_after();
+            const uint32_t d = tmem + (n & 1) * S::kOther + ((uint32_t)(quarter * 32) << 16);
+            const int64_t m = w.m0 + (int)rank * 128 + quarter * 32 + lane;
+            const bool in = m < w.valid;
+            const float xt = MM_XT(p, w.e), alpha = __fmul_rn(xt, MM_WT(p, 0, w.e));
+            const float alpha1 = GATED ? __fmul_rn(xt, MM_WT(p, 1, w.e)) : 0.0f;
+            // runs of 32 columns, the shared ones (5-7 of even tiles, 0-2 of
+            // odd ones) first; the two warps of a quarter take turns
+            constexpr int kRuns = GATED ? 4 : 8;
+#pragma unroll 1
+            for (int j = half; j < kRuns; j += 2) {
+                const int c = (n & 1) ? j : kRuns - 1 - j;
+                float v[32];
+                if constexpr (GATED) {
+                    uint32_t g[32], u[32];
+                    dev::tmem_ld32(d + 32 * c, g);
+                    dev::tmem_ld32(d + 128 + 32 * c, u);
+                    dev::tmem_ld_wait();
+                    if (j == 2 - half) {  // its last run of the first three
+                        dev::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) dev::peer_arrive(drained_bar);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 32; ++q)
+                        v[q] = silu(__uint_as_float(g[q]) * alpha) * (__uint_as_float(u[q]) * alpha1);
+                } else {
+                    uint32_t g[32];
+                    dev::tmem_ld32(d + 32 * c, g);
+                    dev::tmem_ld_wait();
+                    if (j == 2 - half) {  // its last run of the first three
+                        dev::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) dev::peer_arrive(drained_bar);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(g[q]) * alpha;
+                }
+                if (in && w.n0 + 32 * c < p.N) store32<BF16>(p, w.e, m, w.n0 + 32 * c, v);
+            }
+        }
+    }
+    __syncwarp();
+    dev::tc_fence_before();
+    dev::cluster_sync();  // no access to this CTA's memory is left
+    if (warp == 1) dev::tmem_dealloc<2>(tmem, 512);
+}
+
 template <typename K>
 cudaError_t set_smem(K kernel, int smem) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -354,7 +638,33 @@ cudaError_t narrow_format(const Fp4MmParams &p, bool gated, bool bf16, int token
                 : narrow_tokens<FMT, false, false>(p, tokens, st);
 }
 
+template <int FMT, bool GATED, bool BF16>
+cudaError_t wide(const Fp4MmParams &p, cudaStream_t st) {
+    using S = Wide<FMT>;
+    auto kern = k_fp4_wide<FMT, GATED, BF16>;
+    static PerDevice<cudaError_t> setup;
+    const cudaError_t e = setup.get([&] { return set_smem(kern, S::kSmem); });
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (int64_t)((p.M + 255) / 256) * ((p.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256)) *
+                          p.batch;
+    const int64_t pairs = sm_count() / 2;
+    return launch_clusters(kern, dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs))), S::kThreads, 2,
+                           S::kSmem, st, p);
+}
+
+template <int FMT>
+cudaError_t wide_format(const Fp4MmParams &p, bool gated, bool bf16, cudaStream_t st) {
+    if (gated) return bf16 ? wide<FMT, true, true>(p, st) : wide<FMT, true, false>(p, st);
+    return bf16 ? wide<FMT, false, true>(p, st) : wide<FMT, false, false>(p, st);
+}
+
 }  // namespace
+
+cudaError_t launch_fp4_mm_wide(const Fp4MmParams &p, int format, bool gated, bool out_bf16,
+                               cudaStream_t st) {
+    return format == FP8BQ_MXFP4 ? wide_format<FP8BQ_MXFP4>(p, gated, out_bf16, st)
+                                 : wide_format<FP8BQ_NVFP4>(p, gated, out_bf16, st);
+}
 
 int fp4_narrow_tokens(int64_t M, bool gated) {
     for (int t : {16, 32, 64, 128})
