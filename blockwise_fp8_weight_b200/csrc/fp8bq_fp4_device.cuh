@@ -141,6 +141,17 @@ __device__ __forceinline__ void mma_commit_pair_here(uint64_t *bar) {
                      smem_addr(bar)) : "memory");
 }
 
+// 8 columns of this warp's 32 lanes, and the wait for the stores.
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint4 &a, const uint4 &b) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                     addr),
+                 "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- clusters
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -157,9 +168,12 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-// Arrive on a barrier of the cluster (an address from peer_addr).
+// Arrive on a barrier of the cluster (an address from peer_addr).  What it
+// announces is tensor memory, which the tcgen05 fences order; a release at
+// cluster scope would wait for far more (measured: 1 us an arrive while the
+// ring is loading).
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");
 }
 // 3-D TMA tile load into this CTA's shared memory that completes on a barrier

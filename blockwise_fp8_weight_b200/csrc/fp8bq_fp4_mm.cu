@@ -19,7 +19,12 @@ constexpr uint64_t kDrainNs = 2000000000ull;
 
 #define MM_SPAN(base, bytes) (dev::Span{(uint64_t)(base), (uint64_t)(base) + (bytes)})
 
-__device__ __forceinline__ float silu(float v) { return v / (1.0f + expf(-v)); }
+// v / (1 + exp(-v)) by the fast exponential and division: their documented
+// errors are 2 + |1.173 v| and 2 units in the last place, far below the
+// rounding of a bf16 output and of the order of an fp32 sum's own.  (expf and
+// the IEEE division: 313 us instead of 62 for 8192 x 6144 outputs over
+// K = 512, on B200.)
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     uint32_t d;
@@ -298,11 +303,18 @@ __global__ void __launch_bounds__(128) k_fp4_narrow(const __grid_constant__ Fp4M
 // two sums of an output lie 128 columns apart in the same tensor-memory lane.
 //
 // Persistent: a pair walks over tiles.  In each CTA warp 0 loads (one lane),
-// warps 4-11 store; warp 1 of the first CTA issues the products of both.  The
-// sums of successive tiles alternate between columns [0, 256) and [160, 416),
-// so the next tile is multiplied while this one is stored; the 96 columns that
-// both use are stored first, and the next tile waits for those alone.  The
-// scales' two buffers take the last 96 columns.
+// warps 4-7 bring the scales into tensor memory, warps 8-15 store; warp 1 of
+// the first CTA issues the products of both.  The sums of successive tiles
+// alternate between columns [0, 256) and [160, 416), so the next tile is
+// multiplied while this one is stored; the 96 columns that both use are stored
+// first, and the next tile waits for those alone.  The scales' buffers take
+// the last 96 columns.
+//
+// The scales go through registers (ld.shared, tcgen05.st) rather than by
+// tcgen05.cp: a copy of one scale tile holds up the tensor cores for 62
+// clocks, and a stage has 6 (mxfp4) or 12 (nvfp4) of them beside 768 clocks of
+// products.  Measured on B200, 8192 tokens against 6144 x 16384: clocks a
+// stage 1240 / 1570 with the copies.
 template <int FMT>
 struct Wide {
     static constexpr int KT = 256 / (4 * fp4_block(FMT));
@@ -313,9 +325,10 @@ struct Wide {
     static constexpr int kStages = (kSmem - 1024) / kStage;
     static constexpr int kOther = 160;                         // columns of the odd tiles' sums
     static constexpr int kScales = 416;
-    static constexpr int kSfCols = 12 * KT;
-    static constexpr int kThreads = 384;
-    static_assert(2 * kSfCols <= 512 - kScales, "tensor memory");
+    static constexpr int kSfCols = 12 * KT;                    // a stage's: tokens, then weight
+    static constexpr int kSfBufs = (512 - kScales) / kSfCols;
+    static constexpr int kThreads = 512;
+    static_assert(kSfBufs >= 2 && kSfBufs <= kStages, "scale buffers");
 };
 
 // 32 consecutive outputs of a row, from column n; `align` bytes.
@@ -383,11 +396,13 @@ struct WideWalk {
 };
 
 template <int FMT, bool GATED, bool BF16>
-__global__ void __launch_bounds__(384) k_fp4_wide(const __grid_constant__ Fp4MmParams p) {
+__global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4MmParams p) {
     using S = Wide<FMT>;
     extern __shared__ uint8_t raw[];
-    // full, drained: the first CTA's count; empty, sums: each CTA its own
-    __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], sums, drained, done;
+    // full (codes), scaled, drained: the first CTA's count for both; landed
+    // (scales), empty, sums: each CTA its own
+    __shared__ __align__(8) uint64_t full[S::kStages], landed[S::kStages], empty[S::kStages];
+    __shared__ __align__(8) uint64_t scaled[S::kSfBufs], sums, drained, done;
     __shared__ uint32_t tmem_at;
     __shared__ volatile int abort_flag;
     uint8_t *ring = raw + ((1024u - (dev::smem_addr(raw) & 1023u)) & 1023u);
@@ -398,8 +413,10 @@ __global__ void __launch_bounds__(384) k_fp4_wide(const __grid_constant__ Fp4MmP
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             dev::mbar_init(&full[s], 1);
+            dev::mbar_init(&landed[s], 1);
             dev::mbar_init(&empty[s], 1);
         }
+        for (int s = 0; s < S::kSfBufs; ++s) dev::mbar_init(&scaled[s], 8);
         dev::mbar_init(&sums, 1);
         dev::mbar_init(&drained, 16);
         dev::mbar_init(&done, 1);
@@ -437,7 +454,8 @@ __global__ void __launch_bounds__(384) k_fp4_wide(const __grid_constant__ Fp4MmP
                     break;
                 }
                 const uint32_t bar = dev::peer_addr(dev::smem_addr(&full[st]), 0);
-                if (rank == 0) dev::mbar_arrive_expect_tx(&full[st], 2 * S::kStage);
+                if (rank == 0) dev::mbar_arrive_expect_tx(&full[st], 4 * S::kCodes);
+                dev::mbar_arrive_expect_tx(&landed[st], 3 * S::SF);
                 if ((p.inject & FP8BQ_INJECT_DROP_FIRST_LOAD) && i == 0 && blockIdx.x == 0) {
                     dropped = true;
                     continue;
@@ -448,20 +466,23 @@ __global__ void __launch_bounds__(384) k_fp4_wide(const __grid_constant__ Fp4MmP
                 dev::tma_load_3d_pair(b, &p.x, bar, k * 128, w.m0 + (int)rank * 128, at(0));
                 dev::tma_load_3d_pair(b + S::kCodes, &p.w[wi], bar, k * 128, wn, at(2 + 2 * wi));
                 b += 2 * S::kCodes;
-                dev::tma_load_3d_pair(b, &p.xs, bar, k * (S::SF / 8), w.m0 / 128 + (int)rank, at(1));
+                dev::tma_load_3d(b, &p.xs, &landed[st], k * (S::SF / 8), w.m0 / 128 + (int)rank,
+                                 at(1), false);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    dev::tma_load_3d_pair(b + (1 + h) * S::SF, &p.ws[GATED ? h : 0], bar,
-                                          k * (S::SF / 8), w.n0 / 128 + (GATED ? 0 : h),
-                                          at(3 + (GATED ? 2 * h : 0)));
+                    dev::tma_load_3d(b + (1 + h) * S::SF, &p.ws[GATED ? h : 0], &landed[st],
+                                     k * (S::SF / 8), w.n0 / 128 + (GATED ? 0 : h),
+                                     at(3 + (GATED ? 2 * h : 0)), false);
             }
         }
         // Every copy of both CTAs has landed (a dropped stage's others had the
         // whole wait that ran out for it).
-        for (int st = 0; rank == 0 && st < S::kStages && st < i; ++st) {
+        for (int st = 0; st < S::kStages && st < i; ++st) {
             const int fills = (i - st + S::kStages - 1) / S::kStages;
             if (dropped && st == 0 && fills == 1) continue;
-            if (!dev::mbar_wait_bounded(&full[st], (fills - 1) & 1, kDrainNs, nullptr))
+            if ((rank == 0 &&
+                 !dev::mbar_wait_bounded(&full[st], (fills - 1) & 1, kDrainNs, nullptr)) ||
+                !dev::mbar_wait_bounded(&landed[st], (fills - 1) & 1, kDrainNs, nullptr))
                 atomicOr(&g_fp4_error_word, 2u);
         }
     } else if (warp == 1 && lane == 0 && rank == 0) {
@@ -479,25 +500,17 @@ __global__ void __launch_bounds__(384) k_fp4_wide(const __grid_constant__ Fp4MmP
             for (int k = 0; k < p.stages_k; ++k, ++i) {
                 const int st = i % S::kStages;
                 if (!dev::mbar_wait_bounded(&full[st], (i / S::kStages) & 1, p.wait_limit_ns,
-                                            &abort_flag)) {
+                                            &abort_flag) ||
+                    !dev::mbar_wait_bounded(&scaled[i % S::kSfBufs], (i / S::kSfBufs) & 1,
+                                            p.wait_limit_ns, &abort_flag)) {
                     gave_up();
                     ok = false;
                     break;
                 }
                 dev::tc_fence_after();
                 const uint32_t at = dev::smem_addr(ring + st * S::kStage);
-                const uint32_t sf = at + 2 * S::kCodes;
-                const uint32_t sx = tmem + S::kScales + (i & 1) * S::kSfCols;
+                const uint32_t sx = tmem + S::kScales + (i % S::kSfBufs) * S::kSfCols;
                 const uint32_t sw = sx + 4 * S::KT;
-#pragma unroll
-                for (int t = 0; t < S::KT; ++t) {
-                    dev::scales_to_tmem<2>(sx + 4 * t, dev::scale_desc(sf + t * kFp4TileBytes));
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        dev::scales_to_tmem<2>(
-                            sw + 8 * t + 4 * h,
-                            dev::scale_desc(sf + (1 + h) * S::SF + t * kFp4TileBytes));
-                }
                 const uint64_t xd = dev::operand_desc(at), wd = dev::operand_desc(at + S::kCodes);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -514,8 +527,48 @@ __global__ void __launch_bounds__(384) k_fp4_wide(const __grid_constant__ Fp4MmP
         }
         dev::mma_commit_pair_here(&done);
         if (!dev::mbar_wait_bounded(&done, 0, kDrainNs, nullptr)) atomicOr(&g_fp4_error_word, 2u);
-    } else if (warp >= 4) {
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
+    } else if (warp >= 4 && warp < 8) {
+        // Every lane quarter gets the same copy of the scales: lane l of column
+        // c holds the four blocks of row l + 32 c, so a lane's 16 bytes of a
+        // tile are its words of four columns.
+        const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+        bool ok = true;
+        for (int i = 0; ok && w.next();) {
+            for (int k = 0; k < p.stages_k; ++k, ++i) {
+                const int st = i % S::kStages, b = i % S::kSfBufs;
+                bool here = dev::mbar_wait_bounded(&landed[st], (i / S::kStages) & 1,
+                                                   p.wait_limit_ns, &abort_flag);
+                const uint8_t *sf = ring + st * S::kStage + 2 * S::kCodes + lane * 16;
+                uint4 v[3 * S::KT];  // of the tokens, then tile by tile of the weight's two rows
+#pragma unroll
+                for (int t = 0; t < S::KT; ++t) {
+                    v[t] = *(const uint4 *)(sf + t * kFp4TileBytes);
+                    v[S::KT + 2 * t] = *(const uint4 *)(sf + S::SF + t * kFp4TileBytes);
+                    v[S::KT + 2 * t + 1] = *(const uint4 *)(sf + 2 * S::SF + t * kFp4TileBytes);
+                }
+                if (i >= S::kSfBufs) {  // the products that read this buffer are done
+                    const int o = i - S::kSfBufs;
+                    here = here && dev::mbar_wait_bounded(&empty[o % S::kStages],
+                                                          (o / S::kStages) & 1, p.wait_limit_ns,
+                                                          &abort_flag);
+                }
+                if (!__all_sync(0xffffffffu, here)) {
+                    if (lane == 0) gave_up();
+                    ok = false;
+                    break;
+                }
+                dev::tc_fence_after();
+#pragma unroll
+                for (int t = 0; t < 3 * S::KT; t += 2)
+                    dev::tmem_st8(tmem + quarter + S::kScales + b * S::kSfCols + 4 * t, v[t], v[t + 1]);
+                dev::tmem_st_wait();
+                dev::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) dev::peer_arrive(dev::peer_addr(dev::smem_addr(&scaled[b]), 0));
+            }
+        }
+    } else if (warp >= 8) {
+        const int quarter = warp & 3, half = (warp - 8) >> 2;
         const uint32_t drained_bar = dev::peer_addr(dev::smem_addr(&drained), 0);
         for (int n = 0; w.next(); ++n) {
             const bool here =
