@@ -600,8 +600,15 @@ def quant_weights(weights: Iterable, weight_block_size=DEFAULT_BLOCK, stream=Non
 
 
 # ----------------------------------------------------------------- 4-bit conveniences
+#
+# A product of one token takes the GPU a few microseconds, so what these
+# functions do on the host is most of such a call: the descriptor is packed in
+# one call of the struct module, and the checks look at each property once.
 
 _FP4_FORMATS = {"mxfp4": (FP8BQ_MXFP4, 32), "nvfp4": (FP8BQ_NVFP4, 16)}
+# fp8bq_fp4_desc and fp8bq_fp4_matmul_desc as packed bytes
+_FP4_DESC = struct.Struct("<4Q6q2i")
+_FP4_MATMUL_DESC = struct.Struct("<" + 3 * "3Q3q" + "2Q6q2i")
 
 
 def _fp4_format(format: str) -> tuple[int, int]:
@@ -610,6 +617,22 @@ def _fp4_format(format: str) -> tuple[int, int]:
         return _FP4_FORMATS[format]
     except (KeyError, TypeError):
         raise ValueError(f"format must be 'mxfp4' or 'nvfp4', got {format!r}") from None
+
+
+def _fp4_setup(tensor, what: str):
+    """(torch, current device, its current stream) of a call on ``tensor``."""
+    import torch
+    _check_cuda(tensor, what)
+    dev = tensor.get_device()
+    return torch, dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _fp4_empty(shape, dtype, like, stream):
+    """An output on ``like``'s device, allocated on ``stream`` (see _on_stream)."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _on_stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _fp4_tensor_scale(t, batch: int, format: str, what: str) -> tuple[int, int]:
@@ -624,33 +647,32 @@ def _fp4_tensor_scale(t, batch: int, format: str, what: str) -> tuple[int, int]:
     if t.dtype != torch.float32:
         raise TypeError(f"{what} must be float32, got {t.dtype}")
     n = t.numel()
-    if n != 1 and n != batch:
+    if n == 1:
+        return t.data_ptr(), 0
+    if n != batch:
         raise ValueError(f"{what} must hold one value, or one for each of the {batch} matrices")
-    if n > 1 and not t.is_contiguous():
+    if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr(), int(n > 1)
+    return t.data_ptr(), 1
 
 
-def _fp4_shapes(x, block: int):
-    """Shapes of the codes and of the scale tiles of ``x``."""
-    M, K = x.shape[-2], x.shape[-1]
-    return ((*x.shape[:-1], 16 * (-(-K // 32))),
-            (*x.shape[:-2], -(-M // 128), -(-K // (4 * block)), 32, 16))
-
-
-def _fp4_record(w, name: str, format: str, codes: int, scales: int, tensor_scale):
-    """The fields of an ``fp8bq_fp4_desc`` for the tensor ``w``."""
-    _check_cuda(w, name)
-    if w.dim() not in (2, 3):
+def _fp4_record(w, name: str, format: str, block: int, tensor_scale):
+    """(shape of the codes, shape of the scale tiles, the other fields of an
+    ``fp8bq_fp4_desc``) for the CUDA tensor ``w``."""
+    shape = w.shape
+    if len(shape) == 2:
+        (M, K), E, xbs, lead = shape, 1, 0, ()
+    elif len(shape) == 3:
+        E, M, K = shape
+        xbs, lead = w.stride(0), (E,)
+    else:
         raise ValueError(f"{name}: expected a 2-D weight or a 3-D stack of expert weights")
-    M, K = w.shape[-2], w.shape[-1]
     if K > 1 and w.stride(-1) != 1:
         raise ValueError(f"{name}: the last dimension of the input must have unit stride")
-    stack = w.dim() == 3
-    E = w.shape[0] if stack else 1
     t, ts = _fp4_tensor_scale(tensor_scale, E, format, f"{name}'s tensor scale")
-    return (w.data_ptr(), codes, scales, t, M, K, max(w.stride(-2) if M > 1 else K, K), E,
-            w.stride(0) if stack else 0, ts, _dtype_code(w), _FP4_FORMATS[format][0])
+    return ((*lead, M, 16 * (-(-K // 32))), (*lead, -(-M // 128), -(-K // (4 * block)), 32, 16),
+            (t, M, K, max(w.stride(-2), K) if M > 1 else K, E, xbs, ts, _dtype_code(w),
+             _FP4_FORMATS[format][0]))
 
 
 def scaled_fp4_blockwise(data_hp, format="mxfp4", tensor_scale=None, stream=None):
@@ -664,25 +686,17 @@ def scaled_fp4_blockwise(data_hp, format="mxfp4", tensor_scale=None, stream=None
     the block length, in the tiles that the products read (``fp4_scale_rows``
     gives them row by row).  Both are padded with zeros.
     """
-    import torch
-    fmt, block = _fp4_format(format)
-    _check_cuda(data_hp, "data_hp")
-    if data_hp.dim() not in (2, 3):
-        raise ValueError("expected a 2-D weight or a 3-D stack of expert weights")
-    cs, ss = _fp4_shapes(data_hp, block)
-    with _on_stream(stream):
-        codes = torch.empty(cs, dtype=torch.uint8, device=data_hp.device)
-        scales = torch.empty(ss, dtype=torch.uint8, device=data_hp.device)
-    rec = _fp4_record(data_hp, "data_hp", format, codes.data_ptr(), scales.data_ptr(), tensor_scale)
-    check(lib().fp8bq_fp4_quantize_batched(_FP4_DESC.pack(*rec), 1, _stream(stream)),
-          "scaled_fp4_blockwise")
+    _, block = _fp4_format(format)
+    torch, _, current = _fp4_setup(data_hp, "data_hp")
+    cs, ss, rec = _fp4_record(data_hp, "data_hp", format, block, tensor_scale)
+    codes = _fp4_empty(cs, torch.uint8, data_hp, stream)
+    scales = _fp4_empty(ss, torch.uint8, data_hp, stream)
+    st = lib().fp8bq_fp4_quantize_batched(
+        _FP4_DESC.pack(data_hp.data_ptr(), codes.data_ptr(), scales.data_ptr(), *rec), 1,
+        current if stream is None else _stream(stream))
+    if st:
+        check(st, "scaled_fp4_blockwise")
     return codes, scales
-
-
-# fp8bq_fp4_desc and fp8bq_fp4_matmul_desc as packed bytes: one call of the
-# struct module instead of a field at a time.
-_FP4_DESC = struct.Struct("<4Q6q2i")
-_FP4_MATMUL_DESC = struct.Struct("<" + 3 * "3Q3q" + "2Q6q2i")
 
 
 def fp4_scale_rows(scales, rows: int, columns: int, format="mxfp4"):
@@ -700,138 +714,140 @@ def quant_weights_fp4(weights: Iterable, format="mxfp4", stream=None):
     scales) and, for ``"nvfp4"``, (name + "_scale_2", tensor scale) for each
     input, in input order.  The tensor scale is max(max|w|, eps) / (448 * 6),
     so that the largest block's scale is 448."""
-    import torch
-    fmt, block = _fp4_format(format)
+    _, block = _fp4_format(format)
     named = list(weights)
     if not named:
         return []
+    recs = []
     for name, w in named:
         _check_cuda(w, name)
-        if w.dim() not in (2, 3):
-            raise ValueError(f"{name}: expected a 2-D weight or a 3-D stack of expert weights")
-    shapes = [_fp4_shapes(w, block) for _, w in named]
+        recs.append(_fp4_record(w, name, format, block, None))
+    import torch
+    ts = None
     with _on_stream(stream):
-        ts = None
         if format == "nvfp4":
             ts = tensor_scales([w if w.is_contiguous() else w.contiguous() for _, w in named],
                                stream=stream) / 6.0
-        made = [(torch.empty(c, dtype=torch.uint8, device=w.device),
-                 torch.empty(s, dtype=torch.uint8, device=w.device))
-                for (c, s), (_, w) in zip(shapes, named)]
-    recs, out = [], []
-    for i, ((name, w), (codes, scales)) in enumerate(zip(named, made)):
-        t = None if ts is None else ts[i:i + 1]
-        recs.append(_FP4_DESC.pack(*_fp4_record(w, name, format, codes.data_ptr(),
-                                                scales.data_ptr(), t)))
+        made = [(torch.empty(cs, dtype=torch.uint8, device=w.device),
+                 torch.empty(ss, dtype=torch.uint8, device=w.device))
+                for (cs, ss, _), (_, w) in zip(recs, named)]
+    packed, out = [], []
+    for i, ((name, w), (codes, scales), (_, _, rec)) in enumerate(zip(named, made, recs)):
+        if ts is not None:
+            rec = (ts.data_ptr() + 4 * i, *rec[1:])
+        packed.append(_FP4_DESC.pack(w.data_ptr(), codes.data_ptr(), scales.data_ptr(), *rec))
         out += [(name, codes), (name + "_scale", scales)]
-        if t is not None:
-            out.append((name + "_scale_2", t))
-    check(lib().fp8bq_fp4_quantize_batched(b"".join(recs), len(recs), _stream(stream)),
+        if ts is not None:
+            out.append((name + "_scale_2", ts[i:i + 1]))
+    check(lib().fp8bq_fp4_quantize_batched(b"".join(packed), len(packed), _stream(stream)),
           "quant_weights_fp4")
     return out
 
 
-def _fp4_operand(codes, scales, tensor_scale, format: str, block: int, what: str):
-    """The fields of an ``fp8bq_fp4_operand``, and (batch or 0, rows, code bytes a row)."""
-    import torch
-    _check_cuda(codes, what)
-    _check_cuda(scales, f"{what}'s scales")
+def _fp4_operand(torch, dev, codes, scales, tensor_scale, format: str, block: int, what: str):
+    """The fields of an ``fp8bq_fp4_operand``, then its batch (0 for a plain
+    matrix), rows and bytes a row."""
+    if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor) and
+            codes.get_device() == scales.get_device() == dev):
+        _check_cuda(codes, what)
+        _check_cuda(scales, f"{what}'s scales")
     if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise TypeError(f"{what}: codes and scales must be uint8")
-    dim = codes.dim()
-    if dim not in (2, 3) or scales.dim() != dim + 2:
+    shape, ss = codes.shape, scales.shape
+    dim = len(shape)
+    if dim not in (2, 3) or len(ss) != dim + 2:
         raise ValueError(f"{what}: expected codes [(E,) M, K / 2] and scales "
                          "[(E,) M tiles, K tiles, 32, 16]")
-    shape, st = codes.shape, codes.stride()
-    rows, kb = shape[-2], shape[-1]
-    want = (*shape[:-2], -(-rows // 128), -(-2 * kb // (4 * block)), 32, 16)
-    if kb % 16 or tuple(scales.shape) != want:
-        raise ValueError(f"{what}: codes {tuple(shape)} go with {format} scales {want}, "
-                         f"got {tuple(scales.shape)}")
-    ss = scales.stride()
-    if (kb > 1 and st[-1] != 1) or (rows > 1 and st[-2] != kb):
-        raise ValueError(f"{what}: the codes' rows must be contiguous")
-    if ss[-1] != 1 or ss[-2] != 16 or (want[-3] > 1 and ss[-3] != 512) or \
-            (want[-4] > 1 and ss[-4] != 512 * want[-3]):
-        raise ValueError(f"{what}: the scale tiles must be contiguous")
     E = shape[0] if dim == 3 else 0
-    t, ts = _fp4_tensor_scale(tensor_scale, max(E, 1), format, f"{what}'s tensor scale")
-    return ((codes.data_ptr(), scales.data_ptr(), t, st[0] if E else 0, ss[0] if E else 0, ts),
-            (E, rows, kb))
+    rows, kb = shape[-2], shape[-1]
+    mt, kt = -(-rows // 128), -(-kb // (2 * block))
+    if kb % 16 or ss[-4:] != (mt, kt, 32, 16) or (dim == 3 and ss[0] != E):
+        raise ValueError(f"{what}: codes {tuple(shape)} do not go with {format} scales {tuple(ss)}")
+    if codes.is_contiguous() and scales.is_contiguous():
+        cbs, sbs = rows * kb, mt * kt * 512
+    else:
+        cs, st = codes.stride(), scales.stride()
+        if (kb > 1 and cs[-1] != 1) or (rows > 1 and cs[-2] != kb):
+            raise ValueError(f"{what}: the codes' rows must be contiguous")
+        if st[-1] != 1 or st[-2] != 16 or (kt > 1 and st[-3] != 512) or \
+                (mt > 1 and st[-4] != 512 * kt):
+            raise ValueError(f"{what}: the scale tiles must be contiguous")
+        cbs, sbs = cs[0], st[0]
+    t, ts = (0, 0) if tensor_scale is None else \
+        _fp4_tensor_scale(tensor_scale, max(E, 1), format, f"{what}'s tensor scale")
+    return codes.data_ptr(), scales.data_ptr(), t, cbs, sbs, ts, E, rows, kb, dim
 
 
 def dequantize_fp4_blockwise(codes, scales, format="mxfp4", columns=None, tensor_scale=None,
                              out_dtype=None, stream=None):
     """Reverse map of ``scaled_fp4_blockwise``: the values as bf16 (default) or
     fp32, [(E,) M, columns] (default: every column the codes have room for)."""
-    import torch
     fmt, block = _fp4_format(format)
+    torch, dev, current = _fp4_setup(codes, "codes")
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
-    K = 2 * codes.shape[-1] if columns is None else int(columns)
-    if K < 0 or -(-K // 32) * 16 != codes.shape[-1]:
-        raise ValueError(f"codes of {codes.shape[-1]} bytes a row do not hold {K} columns")
-    if K == 0:
-        return torch.empty((*codes.shape[:-1], 0), dtype=out_dtype, device=codes.device)
-    (c, s, t, cbs, sbs, ts), (E, M, kb) = _fp4_operand(codes, scales, tensor_scale, format, block,
-                                                       "codes")
+    c, s, t, cbs, sbs, ts, E, M, kb, dim = _fp4_operand(torch, dev, codes, scales, tensor_scale,
+                                                        format, block, "codes")
+    K = 2 * kb if columns is None else int(columns)
+    if K < 0 or -(-K // 32) * 16 != kb:
+        raise ValueError(f"codes of {kb} bytes a row do not hold {K} columns")
     if E > 1 and (cbs != M * kb or sbs != scales[0].numel()):
         raise ValueError("a stack's codes and scales must be contiguous")
-    with _on_stream(stream):
-        out = torch.empty((*codes.shape[:-1], K), dtype=out_dtype, device=codes.device)
-    check(lib().fp8bq_fp4_dequantize(c, s, E if codes.dim() == 3 else 1, M, K, fmt, t, ts,
-                                     out.data_ptr(),
-                                     FP8BQ_BF16 if out_dtype == torch.bfloat16 else FP8BQ_F32, K,
-                                     M * K, _stream(stream)), "dequantize_fp4_blockwise")
+    out = _fp4_empty((M, K) if dim == 2 else (E, M, K), out_dtype, codes, stream)
+    st = lib().fp8bq_fp4_dequantize(c, s, E if dim == 3 else 1, M, K, fmt, t, ts, out.data_ptr(),
+                                    FP8BQ_BF16 if out_dtype == torch.bfloat16 else FP8BQ_F32, K,
+                                    M * K, current if stream is None else _stream(stream))
+    if st:
+        check(st, "dequantize_fp4_blockwise")
     return out
 
 
-_FP4_NONE = (0, 0, 0, 0, 0, 0)
-
-
-def _fp4_product(entry, a, weights, format, out_dtype, rows, out, stream, what):
-    import torch
+def _fp4_product(entry, a, b, up, format, out_dtype, rows, out, stream, what):
     fmt, block = _fp4_format(format)
-    fa, (E, M, kb) = _fp4_operand(*a, format, block, "a")
-    fields = list(fa)
-    N = -1
-    for name, w in weights:
-        fw, (Ew, n, kw) = _fp4_operand(*w, format, block, name)
-        if Ew != E or kw != kb or N not in (-1, n) or w[0].dim() != a[0].dim():
-            raise ValueError(f"{name}: shape {tuple(w[0].shape)} does not match "
-                             f"a {tuple(a[0].shape)} or the other weight")
-        N = n
-        fields += fw
-    if len(weights) == 1:
-        fields += _FP4_NONE
-    shape = (E, M, N) if a[0].dim() == 3 else (M, N)
+    torch, dev, current = _fp4_setup(a[0], "a")
+    *fa, E, M, kb, dim = _fp4_operand(torch, dev, *a, format, block, "a")
+    *fb, Eb, N, kb_b, dim_b = _fp4_operand(torch, dev, *b, format, block,
+                                           "b" if up is None else "gate")
+    if (Eb, kb_b, dim_b) != (E, kb, dim):
+        raise ValueError(f"a weight {tuple(b[0].shape)} does not match a {tuple(a[0].shape)}")
+    fu = (0, 0, 0, 0, 0, 0)
+    if up is not None:
+        *fu, Eu, Nu, ku, dim_u = _fp4_operand(torch, dev, *up, format, block, "up")
+        if (Eu, Nu, ku, dim_u) != (Eb, N, kb, dim):
+            raise ValueError(f"gate {tuple(b[0].shape)} and up {tuple(up[0].shape)} differ")
+    shape = (E, M, N) if dim == 3 else (M, N)
     if rows is not None:
         _check_cuda(rows, "rows")
-        if a[0].dim() != 3 or rows.dtype != torch.int32 or rows.shape != (E,) or \
-                not rows.is_contiguous():
+        if dim != 3 or rows.dtype != torch.int32 or rows.shape != (E,) or not rows.is_contiguous():
             raise ValueError("rows must be int32, contiguous, one value for each matrix of a stack")
     if out is None:
-        out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
-        if out_dtype not in (torch.bfloat16, torch.float32):
+        if out_dtype is None:
+            out_dtype = torch.bfloat16
+        elif out_dtype not in (torch.bfloat16, torch.float32):
             raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
-        with _on_stream(stream):
-            make = torch.empty if rows is None else torch.zeros
-            out = make(shape, dtype=out_dtype, device=a[0].device)
+        out = _fp4_empty(shape, out_dtype, a[0], stream)
+        if rows is not None:
+            with _on_stream(stream):
+                out.zero_()
+        ld, obs = N, M * N
     else:
         _check_cuda(out, "out")
         if out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
             raise ValueError(f"out must be {shape} {out_dtype or ''}, got {tuple(out.shape)} "
                              f"{out.dtype}")
-        _dtype_code(out)
-        if N > 1 and out.stride(-1) != 1:
+        out_dtype = out.dtype
+        st = out.stride()
+        if N > 1 and st[-1] != 1:
             raise ValueError("the last dimension of out must have unit stride")
-    st = out.stride()
-    fields += (out.data_ptr(), 0 if rows is None else rows.data_ptr(), M, N, 2 * kb,
-               E if len(shape) == 3 else 1, max(st[-2] if M > 1 else N, N),
-               st[0] if len(shape) == 3 else 0, fmt,
-               FP8BQ_BF16 if out.dtype == torch.bfloat16 else FP8BQ_F32)
-    check(entry(_FP4_MATMUL_DESC.pack(*fields), _stream(stream)), what)
+        ld, obs = (max(st[-2], N) if M > 1 else N), (st[0] if dim == 3 else 0)
+    st = entry(_FP4_MATMUL_DESC.pack(
+        *fa, *fb, *fu, out.data_ptr(), 0 if rows is None else rows.data_ptr(), M, N, 2 * kb,
+        E if dim == 3 else 1, ld, obs, fmt,
+        FP8BQ_BF16 if out_dtype == torch.bfloat16 else _dtype_code(out)),
+        current if stream is None else _stream(stream))
+    if st:
+        check(st, what)
     return out
 
 
@@ -848,8 +864,8 @@ def matmul_fp4(a, a_scales, b, b_scales, format="mxfp4", a_tensor_scale=None, b_
     The codes carry no gradient: they are what an inference engine holds.
     """
     return _fp4_product(lib().fp8bq_fp4_matmul, (a, a_scales, a_tensor_scale),
-                        (("b", (b, b_scales, b_tensor_scale)),), format, out_dtype, rows, out,
-                        stream, "matmul_fp4")
+                        (b, b_scales, b_tensor_scale), None, format, out_dtype, rows, out, stream,
+                        "matmul_fp4")
 
 
 def gated_matmul_fp4(a, a_scales, gate, gate_scales, up, up_scales, format="mxfp4",
@@ -860,6 +876,5 @@ def gated_matmul_fp4(a, a_scales, gate, gate_scales, up, up_scales, format="mxfp
     [(E,) 2F, K] weight may be views of it where F is a multiple of 128
     (codes[..., :F, :], scales[..., :F // 128, :, :, :], and the rest)."""
     return _fp4_product(lib().fp8bq_fp4_gated_matmul, (a, a_scales, a_tensor_scale),
-                        (("gate", (gate, gate_scales, gate_tensor_scale)),
-                         ("up", (up, up_scales, up_tensor_scale))), format, out_dtype, rows, out,
-                        stream, "gated_matmul_fp4")
+                        (gate, gate_scales, gate_tensor_scale), (up, up_scales, up_tensor_scale),
+                        format, out_dtype, rows, out, stream, "gated_matmul_fp4")

@@ -290,18 +290,20 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     if (D.batch > 1 && obs < (D.M - 1) * D.ld_out + D.N) return FP8BQ_ERR_OVERLAP;
     Mat mats[3];
     const int n = gated ? 3 : 2;
-    std::vector<Range> ranges;
+    const uintptr_t out_lo = (uintptr_t)D.out, out_hi = out_lo + (uintptr_t)out_bytes;
+    auto in_out = [&](const void *q, __int128 bytes) {
+        return q != nullptr && bytes > 0 && (uintptr_t)q < out_hi &&
+               out_lo < (uintptr_t)q + (uintptr_t)bytes;
+    };
+    bool overlap = in_out(D.rows, (__int128)D.batch * 4);
     for (int i = 0; i < n; ++i) {
         const fp8bq_fp4_operand &o = i == 0 ? D.a : i == 1 ? D.b : D.up;
         const fp8bq_status s = check_operand(o, D, i == 0 ? D.M : D.N, &mats[i]);
         if (s != FP8BQ_OK) return s;
-        add_range(ranges, o.codes, mats[i].code_bytes, false);
-        add_range(ranges, o.scales, mats[i].scale_bytes, false);
-        add_range(ranges, o.tensor_scale, mats[i].t_bytes, false);
+        overlap |= in_out(o.codes, mats[i].code_bytes) || in_out(o.scales, mats[i].scale_bytes) ||
+                   in_out(o.tensor_scale, mats[i].t_bytes);
     }
-    add_range(ranges, D.rows, D.batch * 4, false);
-    add_range(ranges, D.out, out_bytes, true);
-    if (overlaps(ranges)) return FP8BQ_ERR_OVERLAP;
+    if (overlap) return FP8BQ_ERR_OVERLAP;
     const fp8bq_status sd = device_status();
     if (sd != FP8BQ_OK) return sd;
 

@@ -479,3 +479,56 @@ def test_a_wait_that_runs_out_is_reported(M):
         fq.fp8bq_debug_set_wait_limit_ns(0)
     y = fq.matmul_fp4(a, sa, b, sb, "mxfp4", out_dtype=torch.float32)
     assert np.array_equal(as_float(y), va @ vb.T)
+
+
+def test_conveniences_refuse_what_does_not_fit():
+    x = torch.zeros(40, 96, device="cuda", dtype=torch.bfloat16)
+    c, s = fq.scaled_fp4_blockwise(x, "mxfp4")
+    c3, s3 = fq.scaled_fp4_blockwise(torch.stack([x, x]), "mxfp4")
+    t = torch.ones(1, device="cuda")
+    bad = [
+        (ValueError, lambda: fq.scaled_fp4_blockwise(x.t(), "mxfp4")),          # strided columns
+        (ValueError, lambda: fq.scaled_fp4_blockwise(x[0], "mxfp4")),
+        (TypeError, lambda: fq.scaled_fp4_blockwise(x.half(), "mxfp4")),
+        (ValueError, lambda: fq.scaled_fp4_blockwise(x, "mxfp4", tensor_scale=t)),
+        (TypeError, lambda: fq.scaled_fp4_blockwise(x, "nvfp4", tensor_scale=t.double())),
+        (ValueError, lambda: fq.scaled_fp4_blockwise(x, "nvfp4", tensor_scale=t.expand(2))),
+        (ValueError, lambda: fq.dequantize_fp4_blockwise(c, s, "mxfp4", columns=97)),
+        (ValueError, lambda: fq.dequantize_fp4_blockwise(c, s, "mxfp4", columns=64)),
+        (ValueError, lambda: fq.dequantize_fp4_blockwise(c, s, "nvfp4")),       # other tiles
+        (TypeError, lambda: fq.dequantize_fp4_blockwise(c, s, out_dtype=torch.float16)),
+        (TypeError, lambda: fq.dequantize_fp4_blockwise(c.view(torch.int8), s)),
+        (ValueError, lambda: fq.matmul_fp4(c, s, c[:, :32], s)),
+        (ValueError, lambda: fq.matmul_fp4(c, s, c3, s3)),                      # a stack with a matrix
+        (ValueError, lambda: fq.matmul_fp4(c[::2], s, c, s)),                   # rows apart
+        (ValueError, lambda: fq.matmul_fp4(c, s, c, s[:, :, :16])),
+        (ValueError, lambda: fq.gated_matmul_fp4(c, s, c, s, c[:32], s)),       # gate and up differ
+        (ValueError, lambda: fq.matmul_fp4(c, s, c, s, rows=torch.ones(1, device="cuda").int())),
+        (ValueError, lambda: fq.matmul_fp4(c3, s3, c3, s3, rows=torch.ones(2, device="cuda"))),
+        (ValueError, lambda: fq.matmul_fp4(c3, s3, c3, s3, rows=torch.ones(2).int())),
+        (TypeError, lambda: fq.matmul_fp4(c, s, c, s, out_dtype=torch.float16)),
+        (ValueError, lambda: fq.matmul_fp4(c, s, c, s, out=x)),
+        (TypeError, lambda: fq.matmul_fp4(c, s, c, s, out=torch.empty(40, 40, device="cuda").half())),
+        (ValueError, lambda: fq.matmul_fp4(c, s, c, s, out=torch.empty(40, 80, device="cuda")[:, ::2])),
+        (ValueError, lambda: fq.matmul_fp4(c, s, c, s, "mxfp4", a_tensor_scale=t)),
+        (fq.Fp8bqError, lambda: fq.matmul_fp4(c3, s3, c3, s3, out=torch.empty(
+            1, 40, 40, device="cuda").expand(2, 40, 40))),                      # outputs overlap
+        (fq.Fp8bqError, lambda: fq.matmul_fp4(c[:, :0], s[:, :0], c[:, :0], s[:, :0])),   # empty sums
+    ]
+    for i, (error, call) in enumerate(bad):
+        with pytest.raises(error):
+            call()
+            pytest.fail(f"call {i} was not refused")
+
+
+def test_empty_inputs():
+    for shape in ((0, 64), (3, 0), (0, 5, 64), (2, 0, 64)):
+        x = torch.zeros(shape, device="cuda")
+        c, s = fq.scaled_fp4_blockwise(x, "nvfp4")
+        y = fq.dequantize_fp4_blockwise(c, s, "nvfp4", columns=shape[-1])
+        assert y.shape == shape
+    c, s = fq.scaled_fp4_blockwise(torch.zeros(0, 64, device="cuda"))
+    w, ws = fq.scaled_fp4_blockwise(torch.ones(16, 64, device="cuda"))
+    assert fq.matmul_fp4(c, s, w, ws).shape == (0, 16)
+    assert fq.matmul_fp4(w, ws, c, s).shape == (16, 0)
+    assert fq.quant_weights_fp4([]) == []
