@@ -64,12 +64,12 @@ constexpr int kMaxFp4Large = FP8BQ_CHECKED ? 224 : 288;
 static_assert(sizeof(Fp4Pack<kMaxFp4Large>) < 32000, "kernel parameter limit");
 
 // align: bytes of the widest access every row of the high-precision side
-// allows (16, 8 or the element's size)
+// allows (32, 16, 8 or the element's size)
 template <int MAXD>
 cudaError_t launch_fp4_quantize(const Fp4Pack<MAXD> &p, int format, int esize, int align,
                                 cudaStream_t st);
 template <int MAXD>
-cudaError_t launch_fp4_dequantize(const Fp4Pack<MAXD> &p, int format, int esize, bool vector,
+cudaError_t launch_fp4_dequantize(const Fp4Pack<MAXD> &p, int format, int esize, int align,
                                   cudaStream_t st);
 
 // ------------------------------------------------------------------ products

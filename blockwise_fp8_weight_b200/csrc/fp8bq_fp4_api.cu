@@ -112,7 +112,7 @@ void fill(const Stack &D, bool x_is_output, uint64_t begin, Fp4Desc *o) {
 // Bytes of the widest access that every row of the high-precision side allows.
 int align_of(const Stack &D) {
     const int es = esize_of(D.dtype);
-    for (int a : {16, 8})
+    for (int a : {32, 16, 8})
         if ((uintptr_t)D.x % a == 0 && (D.ld * es) % a == 0 && (D.xbs * es) % a == 0) return a;
     return es;
 }
@@ -152,7 +152,7 @@ fp8bq_status run_quantize(std::vector<Stack> &t, cudaStream_t stream) {
         add_range(ranges, t[i].scales, t[i].scale_bytes(), true);
         add_range(ranges, t[i].tscale, t[i].t_bytes(), false);
         const int a = align_of(t[i]);
-        groups[t[i].format][t[i].dtype == FP8BQ_F32][a == 16 ? 0 : a == 8 ? 1 : 2].push_back((int)i);
+        groups[t[i].format][t[i].dtype == FP8BQ_F32][a >= 16 ? 0 : a == 8 ? 1 : 2].push_back((int)i);
     }
     if (!any) return FP8BQ_OK;
     if (overlaps(ranges)) return FP8BQ_ERR_OVERLAP;
@@ -196,11 +196,8 @@ fp8bq_status run_dequantize(Stack D, cudaStream_t stream) {
     p.n = 1;
     fill(D, true, 0, &p.d[0]);
     p.total = p.d[0].items;
-    // eight outputs a store: 16 bytes of bf16, 32 of fp32
-    const int es = esize_of(D.dtype), a = 8 * es;
-    const bool vector =
-        (uintptr_t)D.x % a == 0 && (D.ld * es) % a == 0 && (D.xbs * es) % a == 0;
-    if (launch_fp4_dequantize<kMaxDescSmall>(p, D.format, es, vector, stream) != cudaSuccess) {
+    if (launch_fp4_dequantize<kMaxDescSmall>(p, D.format, esize_of(D.dtype), align_of(D), stream) !=
+        cudaSuccess) {
         cudaGetLastError();
         return FP8BQ_ERR_DEVICE;
     }
