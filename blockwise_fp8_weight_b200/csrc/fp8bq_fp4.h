@@ -35,9 +35,10 @@ inline int64_t fp4_tiles_k(int64_t K, int format) {
 // ------------------------------------------------------------------ quantise, dequantise
 //
 // A work item is a warp's: rows r, r + 32, r + 64 and r + 96 of a 128-row
-// tile row by 256 columns, so that the scales of an item fill whole 16-byte
-// runs of the tiles.
-constexpr int kFp4ItemCols = 256;
+// tile row by a run of columns, so that the scales of an item fill whole
+// 16-byte runs of the tiles.  The run: 32 bytes a lane of the high-precision
+// side.
+constexpr int fp4_item_cols(int esize) { return 32 * (32 / esize); }
 
 struct Fp4Desc {
     const void *x;       // high-precision side: input, or output of dequantise

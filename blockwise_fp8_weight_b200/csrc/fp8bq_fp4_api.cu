@@ -97,8 +97,8 @@ void fill(const Stack &D, bool x_is_output, uint64_t begin, Fp4Desc *o) {
     o->tiles_m = (int32_t)fp4_tiles_m(D.M);
     o->tiles_k = (int32_t)fp4_tiles_k(D.K, D.format);
     o->begin = begin;
-    o->items = (uint64_t)D.batch * fp4_tiles_m(D.M) * 32 *
-               (uint64_t)((D.K + kFp4ItemCols - 1) / kFp4ItemCols);
+    const int64_t cols = fp4_item_cols(esize_of(D.dtype));
+    o->items = (uint64_t)D.batch * fp4_tiles_m(D.M) * 32 * (uint64_t)((D.K + cols - 1) / cols);
 #if FP8BQ_CHECKED
     o->x_bytes = x_is_output ? checked_extent(D.x_bytes()) : D.x_bytes();
     o->codes_bytes = x_is_output ? D.code_bytes() : checked_extent(D.code_bytes());
@@ -138,8 +138,8 @@ cudaError_t quantize_group(const std::vector<Stack> &t, const std::vector<int> &
 
 fp8bq_status run_quantize(std::vector<Stack> &t, cudaStream_t stream) {
     std::vector<Range> ranges;
-    std::vector<int> groups[2][2][3];  // format, fp32 input, alignment
-    static constexpr int kAligns[3] = {16, 8, 0};
+    std::vector<int> groups[2][2][4];  // format, fp32 input, alignment
+    static constexpr int kAligns[4] = {32, 16, 8, 0};
     bool any = false;
     for (size_t i = 0; i < t.size(); ++i) {
         bool empty = false;
@@ -152,7 +152,7 @@ fp8bq_status run_quantize(std::vector<Stack> &t, cudaStream_t stream) {
         add_range(ranges, t[i].scales, t[i].scale_bytes(), true);
         add_range(ranges, t[i].tscale, t[i].t_bytes(), false);
         const int a = align_of(t[i]);
-        groups[t[i].format][t[i].dtype == FP8BQ_F32][a >= 16 ? 0 : a == 8 ? 1 : 2].push_back((int)i);
+        groups[t[i].format][t[i].dtype == FP8BQ_F32][a == 32 ? 0 : a == 16 ? 1 : a == 8 ? 2 : 3].push_back((int)i);
     }
     if (!any) return FP8BQ_OK;
     if (overlaps(ranges)) return FP8BQ_ERR_OVERLAP;
@@ -160,7 +160,7 @@ fp8bq_status run_quantize(std::vector<Stack> &t, cudaStream_t stream) {
     if (sd != FP8BQ_OK) return sd;
     for (auto &by_format : groups)
         for (auto &by_type : by_format)
-            for (int a = 0; a < 3; ++a) {
+            for (int a = 0; a < 4; ++a) {
                 const std::vector<int> &g = by_type[a];
                 if (g.empty()) continue;
                 const cudaError_t e = g.size() <= (size_t)kMaxDescSmall

@@ -39,16 +39,18 @@ __device__ __forceinline__ int first_desc(const Fp4Pack<MAXD> &p, uint64_t k) {
     return lo;
 }
 
-// A warp's work item: tile row (of the whole stack), row in it, column run.
+// A warp's work item: tile row (of the whole stack), row in it, run of COLS
+// columns.
 struct Item {
     int64_t b;          // matrix of the stack
     int64_t tile_row;   // over the stack
     int32_t row0;       // first of its four rows (32 apart), within the matrix
     int32_t r;          // row0 % 32
-    int32_t seg;        // 256-column run
+    int32_t seg;        // column run
 };
+template <int COLS>
 __device__ __forceinline__ Item item_of(const Fp4Desc &a, uint64_t k) {
-    const uint32_t segs = ((uint32_t)a.K + kFp4ItemCols - 1) / kFp4ItemCols;
+    const uint32_t segs = ((uint32_t)a.K + COLS - 1) / COLS;
     const uint64_t local = k - a.begin;
     Item it;
     uint64_t lr;
@@ -68,32 +70,41 @@ __device__ __forceinline__ Item item_of(const Fp4Desc &a, uint64_t k) {
 
 // ------------------------------------------------------------------ quantise
 
-// A lane's eight consecutive elements of a row, zero beyond `n`, in 4 (bf16,
-// two a word) or 8 words.  ALIGN: 16 or 8, which every row is aligned to.
+// A lane's N consecutive elements of a row (N * ES = 32 bytes), zero beyond
+// `n`, bf16 two a word.  ALIGN: 32, 16 or 8, which every row is aligned to.
+// With less than 32 the lane's accesses share sectors, which L1 then keeps.
 template <int ES, int ALIGN>
-__device__ __forceinline__ void load8(const char *p, int n, uint32_t (&v)[2 * ES],
-                                      [[maybe_unused]] const dev::Span &xs) {
-    if (n >= 8) {
-        if constexpr (ALIGN == 16) {
+__device__ __forceinline__ void load32(const char *p, int n, uint32_t (&v)[8],
+                                       [[maybe_unused]] const dev::Span &xs) {
+    constexpr int N = 32 / ES;
+    if (n >= N) {
+        if (!FP8BQ_IN(xs, p, 32)) {
 #pragma unroll
-            for (int i = 0; i < ES / 2; ++i) {
-                const uint4 q = FP8BQ_IN(xs, p + 16 * i, 16) ? dev::ldg_stream_v4(p + 16 * i)
-                                                             : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 8; ++i) v[i] = 0;
+        } else if constexpr (ALIGN == 32) {
+            asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v8.b32 "
+                         "{%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                           "=r"(v[6]), "=r"(v[7])
+                         : "l"(p));
+        } else if constexpr (ALIGN == 16) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint4 q = __ldg((const uint4 *)(p + 16 * i));
                 v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < ES; ++i) {
-                const uint2 q = FP8BQ_IN(xs, p + 8 * i, 8) ? dev::ldg_v2(p + 8 * i)
-                                                           : make_uint2(0u, 0u);
+            for (int i = 0; i < 4; ++i) {
+                const uint2 q = dev::ldg_v2(p + 8 * i);
                 v[2 * i] = q.x, v[2 * i + 1] = q.y;
             }
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 2 * ES; ++i) v[i] = 0;
+        for (int i = 0; i < 8; ++i) v[i] = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < N; ++i)
             if (i < n && FP8BQ_IN(xs, p + i * ES, ES)) {
                 if constexpr (ES == 2)
                     v[i / 2] |= (uint32_t)__ldg((const unsigned short *)p + i) << (16 * (i & 1));
@@ -103,13 +114,13 @@ __device__ __forceinline__ void load8(const char *p, int n, uint32_t (&v)[2 * ES
     }
 }
 
-// The same for rows of any alignment: the warp's 256 columns by element, so
+// The same for rows of any alignment: the warp's 1024 bytes by element, so
 // that a load instruction covers consecutive addresses, through shared memory.
 template <int ES>
 __device__ __forceinline__ void load_by_element(const char *row, int lane, int n, char *buf,
                                                 [[maybe_unused]] const dev::Span &xs) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 32 / ES; ++j) {
         const int c = 32 * j + lane;
         const bool in = c < n && FP8BQ_IN(xs, row + c * ES, ES);
         if constexpr (ES == 2)
@@ -132,14 +143,10 @@ __device__ __forceinline__ uint32_t amax_f32(uint32_t a, uint32_t b) {
 }
 
 // Eight codes of x * r, element 0 in the low four bits.
-template <int ES>
-__device__ __forceinline__ uint32_t codes8(const uint32_t (&w)[2 * ES], float r) {
-    uint32_t v[8], o;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if constexpr (ES == 2) v[i] = (i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16;
-        else v[i] = w[i];
-    }
+__device__ __forceinline__ uint32_t codes8(uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3,
+                                           uint32_t v4, uint32_t v5, uint32_t v6, uint32_t v7,
+                                           float r) {
+    uint32_t o;
     asm("{\n\t.reg .b64 rr, a, b, c, d;\n\t.reg .f32 l, h;\n\t.reg .b8 p, q, s, t;\n\t"
         "mov.b64 rr, {%9, %9};\n\t"
         "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
@@ -152,9 +159,13 @@ __device__ __forceinline__ uint32_t codes8(const uint32_t (&w)[2 * ES], float r)
         "mov.b64 {l, h}, d;\n\tcvt.rn.satfinite.e2m1x2.f32 t, h, l;\n\t"
         "mov.b32 %0, {p, q, s, t};\n\t}"
         : "=r"(o)
-        : "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-          "f"(r));
+        : "r"(v0), "r"(v1), "r"(v2), "r"(v3), "r"(v4), "r"(v5), "r"(v6), "r"(v7), "f"(r));
     return o;
+}
+// The codes of a lane's 32 bytes: 16 bf16 (two words of codes) or 8 fp32 (one).
+__device__ __forceinline__ uint32_t codes_bf16(const uint32_t *w, float r) {
+    return codes8(w[0] << 16, w[0] & 0xffff0000u, w[1] << 16, w[1] & 0xffff0000u, w[2] << 16,
+                  w[2] & 0xffff0000u, w[3] << 16, w[3] & 0xffff0000u, r);
 }
 
 // Scale byte and multiplier of a block from the bits of its absmax; -0 as the
@@ -182,23 +193,27 @@ __device__ __forceinline__ uint32_t block_scale4(uint32_t amax, float t, float &
     return bad ? (FMT == FP8BQ_MXFP4 ? 0xffu : 0x7fu) : s;
 }
 
-// A block is LPB lanes of a row.  The four rows' maxima are reduced and handed
-// out at once: each lane of a block ends with the block's maximum in 4 / LPB
-// of the rows (row lane % 4, or rows 2 (lane % 2) and the next), finds those
-// scales alone and passes the multipliers on.  Its scale bytes, joined over
-// the tile's four blocks, are then the words of its rows in the tile's 16-byte
-// run.
+// A lane holds 32 bytes of each of its four rows, so a block is LPB = 1, 2 or
+// 4 lanes of a row.  Where it is more than one, the rows' maxima are reduced
+// and handed out at once: each lane of a block ends with the block's maximum
+// in R = 4 / LPB of the rows (rows R (lane % LPB) and the next), finds those
+// scales alone and passes the multipliers on.  The scale bytes of a tile's
+// four blocks are then joined into the words of its rows in the tile's
+// 16-byte run.
 //
-// Measured on B200, 12288 x 4096 bf16, mxfp4: 23.6 us (5.4 TB/s); 39 us with
-// every lane reducing and scaling all four rows, 64-bit divisions for the
-// item's place and the maxima taken element by element.
+// Measured on B200, 12288 x 4096 bf16: mxfp4 20.5 us (6.2 TB/s), nvfp4 23.0
+// (5.6; 25.3 with three CTAs an SM, 24.4 with five); 65536 x 4096 mxfp4 98.6
+// (6.9 TB/s).  16 bytes a lane and row: 23.7, 30.3, 115.8; every lane reducing
+// and scaling all four rows as well: 39.
 template <int FMT, int ES, int ALIGN, int MAXD>
-__global__ void __launch_bounds__(256) k_fp4_quant(const __grid_constant__ Fp4Pack<MAXD> p) {
+__global__ void __launch_bounds__(256, 4) k_fp4_quant(const __grid_constant__ Fp4Pack<MAXD> p) {
     dev::pdl_entry();
-    constexpr int LPB = FMT == FP8BQ_MXFP4 ? 4 : 2;    // lanes a block
+    constexpr int N = 32 / ES;                         // elements of a lane
+    constexpr int LPB = fp4_block(FMT) / N;            // lanes a block
+    constexpr int R = 4 / LPB;                         // rows whose scales a lane finds
     constexpr int TL = 4 * LPB;                        // lanes a tile
     constexpr bool kByElement = ALIGN < 8;
-    __shared__ __align__(16) char stage[kByElement ? 8 : 1][4][kByElement ? 256 * ES : 16];
+    __shared__ __align__(16) char stage[kByElement ? 8 : 1][4][kByElement ? 1024 : 16];
     const int lane = threadIdx.x & 31;
     const uint64_t warps = (uint64_t)gridDim.x * (blockDim.x >> 5);
     const uint64_t k0 = (uint64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -206,8 +221,8 @@ __global__ void __launch_bounds__(256) k_fp4_quant(const __grid_constant__ Fp4Pa
     for (uint64_t k = k0; k < p.total; k += warps) {
         while (k >= p.d[d].begin + p.d[d].items) ++d;
         const Fp4Desc &a = p.d[d];
-        const Item it = item_of(a, k);
-        const int s0 = it.seg * kFp4ItemCols, c0 = s0 + lane * 8;
+        const Item it = item_of<32 * N>(a, k);
+        const int s0 = it.seg * 32 * N, c0 = s0 + lane * N;
         const int n = a.K - c0;                        // columns of this lane that exist
         const int64_t kb = (int64_t)((a.K + 31) >> 5) * 16;
 #if FP8BQ_CHECKED
@@ -215,10 +230,10 @@ __global__ void __launch_bounds__(256) k_fp4_quant(const __grid_constant__ Fp4Pa
 #else
         constexpr dev::Span xs{0, 0};
 #endif
-        uint32_t v[4][2 * ES];
+        uint32_t v[4][8];
         if constexpr (kByElement) {
             const char *x = (const char *)a.x + (it.b * a.xbs + it.row0 * a.ld + s0) * ES;
-            char(*buf)[256 * ES] = stage[threadIdx.x >> 5];
+            char(*buf)[1024] = stage[threadIdx.x >> 5];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 load_by_element<ES>(x + (int64_t)(32 * i) * a.ld * ES, lane,
@@ -227,8 +242,8 @@ __global__ void __launch_bounds__(256) k_fp4_quant(const __grid_constant__ Fp4Pa
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < ES / 2; ++j) {
-                    const uint4 q = *(const uint4 *)(buf[i] + (lane * 8) * ES + 16 * j);
+                for (int j = 0; j < 2; ++j) {
+                    const uint4 q = *(const uint4 *)(buf[i] + lane * 32 + 16 * j);
                     v[i][4 * j] = q.x, v[i][4 * j + 1] = q.y;
                     v[i][4 * j + 2] = q.z, v[i][4 * j + 3] = q.w;
                 }
@@ -237,34 +252,35 @@ __global__ void __launch_bounds__(256) k_fp4_quant(const __grid_constant__ Fp4Pa
             const char *x = (const char *)a.x + (it.b * a.xbs + it.row0 * a.ld + c0) * ES;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                load8<ES, ALIGN>(x + (int64_t)(32 * i) * a.ld * ES,
-                                 it.row0 + 32 * i < a.M ? n : 0, v[i], xs);
+                load32<ES, ALIGN>(x + (int64_t)(32 * i) * a.ld * ES,
+                                  it.row0 + 32 * i < a.M ? n : 0, v[i], xs);
         }
         float t = 1.0f;
         if (FMT == FP8BQ_NVFP4 && a.tscale != nullptr &&
             FP8BQ_IN(FP4_SPAN_T(a), a.tscale + it.b * a.tbs, 4))
             t = __ldg(a.tscale + it.b * a.tbs);
 
-        // maxima of the lane's rows: m[0] (and m[1]) after the exchange
+        // m[h], h < R: the block's maximum (fp32 bits) in row R (lane % LPB) + h
         uint32_t m[4];
         if constexpr (ES == 2) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                m[i] = amax_bf16x2(amax_bf16x2(v[i][0], v[i][1]), amax_bf16x2(v[i][2], v[i][3]));
-            const uint32_t lo =
+                m[i] = amax_bf16x2(amax_bf16x2(amax_bf16x2(v[i][0], v[i][1]),
+                                               amax_bf16x2(v[i][2], v[i][3])),
+                                   amax_bf16x2(amax_bf16x2(v[i][4], v[i][5]),
+                                               amax_bf16x2(v[i][6], v[i][7])));
+            uint32_t lo =
                 amax_bf16x2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
             const uint32_t hi =
                 amax_bf16x2(__byte_perm(m[2], m[3], 0x5410), __byte_perm(m[2], m[3], 0x7632));
-            const bool up = lane & (LPB / 2);          // keeps rows 2 and 3
-            uint32_t w = amax_bf16x2(up ? hi : lo,
-                                     __shfl_xor_sync(0xffffffffu, up ? lo : hi, LPB / 2));
-            if constexpr (LPB == 4) {
-                w = amax_bf16x2(w, __shfl_xor_sync(0xffffffffu, w, 1));
-                m[0] = ((lane & 1) ? w & 0xffff0000u : w << 16) & 0x7fffffffu;
-            } else {
-                m[0] = (w << 16) & 0x7fffffffu;
-                m[1] = w & 0x7fff0000u;
+            if constexpr (LPB == 2) {
+                const bool up = lane & 1;              // keeps rows 2 and 3
+                lo = amax_bf16x2(up ? hi : lo, __shfl_xor_sync(0xffffffffu, up ? lo : hi, 1));
             }
+            m[0] = (lo << 16) & 0x7fffffffu;
+            m[1] = lo & 0x7fff0000u;
+            m[2] = (hi << 16) & 0x7fffffffu;
+            m[3] = hi & 0x7fff0000u;
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -282,41 +298,61 @@ __global__ void __launch_bounds__(256) k_fp4_quant(const __grid_constant__ Fp4Pa
             m[0] &= 0x7fffffffu;
             m[1] &= 0x7fffffffu;
         }
-        uint32_t s[4 / LPB];
-        float mine[4 / LPB], r[4];
+        uint32_t s[R];
+        float mine[R], r[4];
 #pragma unroll
-        for (int h = 0; h < 4 / LPB; ++h) s[h] = block_scale4<FMT>(m[h], t, mine[h]);
+        for (int h = 0; h < R; ++h) s[h] = block_scale4<FMT>(m[h], t, mine[h]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            r[i] = __shfl_sync(0xffffffffu, mine[i % (4 / LPB)],
-                               lane - lane % LPB + i / (4 / LPB));
+            r[i] = LPB == 1 ? mine[i % R]
+                            : __shfl_sync(0xffffffffu, mine[i % R], lane - lane % LPB + i / R);
 
         uint8_t *codes = a.codes + (it.b * a.M + it.row0) * kb + (c0 >> 1);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t c = codes8<ES>(v[i], r[i]);
-            if (__float_as_uint(r[i]) == 0x80000000u) c = 0;   // inf * 0 would be NaN
+            // a block that is not finite: inf * 0 would be NaN
+            const uint32_t keep = __float_as_uint(r[i]) == 0x80000000u ? 0u : ~0u;
             uint8_t *dst = codes + (int64_t)(32 * i) * kb;
-            if (it.row0 + 32 * i < a.M && c0 < 2 * kb && FP8BQ_IN(FP4_SPAN_C(a), dst, 4))
-                dev::stg_stream_u32(dst, c);
+            const bool in = it.row0 + 32 * i < a.M && c0 < 2 * kb && FP8BQ_IN(FP4_SPAN_C(a), dst, N / 2);
+            if constexpr (ES == 2) {
+                const uint2 c = make_uint2(codes_bf16(v[i], r[i]) & keep,
+                                           codes_bf16(v[i] + 4, r[i]) & keep);
+                if (in) dev::stg_stream_v2(dst, c);
+            } else {
+                const uint32_t c = codes8(v[i][0], v[i][1], v[i][2], v[i][3], v[i][4], v[i][5],
+                                          v[i][6], v[i][7], r[i]) & keep;
+                if (in) dev::stg_stream_u32(dst, c);
+            }
         }
 
         const int blk = (lane % TL) / LPB;
         const int tile = it.seg * (32 / TL) + lane / TL;
-        const int i0 = lane % LPB * (4 / LPB);         // this lane's (first) row
-        uint8_t *run =
-            a.scales + (it.tile_row * a.tiles_k + tile) * kFp4TileBytes + it.r * 16 + 4 * i0;
-        const bool exists = (c0 & ~(8 * LPB - 1)) < a.K;   // the block's first column does
-        uint32_t w[4 / LPB];
+        const int i0 = lane % LPB * R;                 // this lane's first row
+        uint8_t *run = a.scales + (it.tile_row * a.tiles_k + tile) * kFp4TileBytes + it.r * 16;
+        const bool exists = (c0 & ~(N * LPB - 1)) < a.K;   // the block's first column does
 #pragma unroll
-        for (int h = 0; h < 4 / LPB; ++h) {
-            w[h] = exists && it.row0 + 32 * (i0 + h) < a.M ? s[h] << (8 * blk) : 0u;
+        for (int h = 0; h < R; ++h)
+            if (!exists || it.row0 + 32 * (i0 + h) >= a.M) s[h] = 0;
+        if constexpr (LPB == 1) {  // a 4 x 4 transpose of bytes: lane `blk` gets row blk's word
+            const uint32_t q = s[0] | s[1 % R] << 8 | s[2 % R] << 16 | s[3 % R] << 24;
+            const uint32_t q2 = __shfl_xor_sync(0xffffffffu, q, 2);
+            const uint32_t u = (lane & 2) ? __byte_perm(q2, q, 0x7632) : __byte_perm(q, q2, 0x5410);
+            const uint32_t u2 = __shfl_xor_sync(0xffffffffu, u, 1);
+            const uint32_t w = (lane & 1) ? __byte_perm(u2, u, 0x7351) : __byte_perm(u, u2, 0x6240);
+            if (tile < a.tiles_k && FP8BQ_IN(FP4_SPAN_S(a), run + 4 * blk, 4))
+                *(uint32_t *)(run + 4 * blk) = w;
+        } else {
+            uint32_t w[R];
 #pragma unroll
-            for (int o = LPB; o < TL; o *= 2) w[h] |= __shfl_xor_sync(0xffffffffu, w[h], o);
-        }
-        if (blk == 0 && tile < a.tiles_k && FP8BQ_IN(FP4_SPAN_S(a), run, 16 / LPB)) {
-            if constexpr (LPB == 4) *(uint32_t *)run = w[0];
-            else *(uint2 *)run = make_uint2(w[0], w[1]);
+            for (int h = 0; h < R; ++h) {
+                w[h] = s[h] << (8 * blk);
+#pragma unroll
+                for (int o = LPB; o < TL; o *= 2) w[h] |= __shfl_xor_sync(0xffffffffu, w[h], o);
+            }
+            if (blk == 0 && tile < a.tiles_k && FP8BQ_IN(FP4_SPAN_S(a), run + 4 * i0, 4 * R)) {
+                if constexpr (R == 1) *(uint32_t *)(run + 4 * i0) = w[0];
+                else *(uint2 *)(run + 4 * i0) = make_uint2(w[0], w[1 % R]);
+            }
         }
     }
 }
@@ -352,13 +388,9 @@ __device__ __forceinline__ float scale_value(uint32_t s) {
     }
 }
 
-// Rows that do not allow a lane's whole run of eight outputs (fp32: 32 bytes)
-// pass through shared memory: the warp's 256 outputs go out in pieces of W
-// bytes, piece j * 32 + lane by lane, so that a store instruction covers
-// consecutive addresses and fills its sectors.  Measured on B200, 4000 x 4100
-// to fp32 (16-byte aligned rows): 14.2 us against 18.9 with two 16-byte stores
-// 32 bytes apart.  (8-byte aligned bf16 rows are the other way round: 8.7 us
-// with two 8-byte stores, 10.8 through shared memory.)
+// Rows that are not 32-byte aligned pass through shared memory: the warp's
+// 1024 bytes go out in pieces of W bytes, piece j * 32 + lane by lane, so that
+// a store instruction covers consecutive addresses and fills its sectors.
 template <int W> struct Piece;
 template <> struct Piece<16> { using T = uint4; };
 template <> struct Piece<8> { using T = uint2; };
@@ -371,7 +403,7 @@ __device__ __forceinline__ void stage_to_row(const char *buf, int lane, int n, c
     using P = typename Piece<W>::T;
     constexpr int E = W / OES;
 #pragma unroll
-    for (int j = 0; j < 256 / E / 32; ++j) {
+    for (int j = 0; j < 32 / W; ++j) {
         const int c = (32 * j + lane) * E;
         if (c + E <= n) {
             if (FP8BQ_IN(xs, row + c * OES, W)) *(P *)(row + c * OES) = *(const P *)(buf + c * OES);
@@ -388,15 +420,16 @@ __device__ __forceinline__ void stage_to_row(const char *buf, int lane, int n, c
     }
 }
 
-// ALIGN: bytes (32 for fp32, 16, 8, or the element's) that every output row is
-// aligned to.
+// ALIGN: bytes (32, 16, 8, or the element's) that every output row is aligned
+// to.
 template <int FMT, int OES, int ALIGN, int MAXD>
 __global__ void __launch_bounds__(256) k_fp4_dequant(const __grid_constant__ Fp4Pack<MAXD> p) {
     dev::pdl_entry();
-    constexpr int LPB = FMT == FP8BQ_MXFP4 ? 4 : 2;
+    constexpr int N = 32 / OES;                        // outputs of a lane
+    constexpr int LPB = fp4_block(FMT) / N;
     constexpr int TL = 4 * LPB;
-    constexpr bool kStaged = ALIGN < (OES == 4 ? 32 : 8);
-    __shared__ __align__(16) char stage[kStaged ? 8 : 1][kStaged ? 256 * OES : 16];
+    constexpr bool kStaged = ALIGN < 32;
+    __shared__ __align__(16) char stage[kStaged ? 8 : 1][kStaged ? 1024 : 16];
     const int lane = threadIdx.x & 31;
     const uint64_t warps = (uint64_t)gridDim.x * (blockDim.x >> 5);
     const uint64_t k0 = (uint64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -404,18 +437,25 @@ __global__ void __launch_bounds__(256) k_fp4_dequant(const __grid_constant__ Fp4
     for (uint64_t k = k0; k < p.total; k += warps) {
         while (k >= p.d[d].begin + p.d[d].items) ++d;
         const Fp4Desc &a = p.d[d];
-        const Item it = item_of(a, k);
-        const int c0 = it.seg * kFp4ItemCols + lane * 8;
+        const Item it = item_of<32 * N>(a, k);
+        const int c0 = it.seg * 32 * N + lane * N;
         const int n = a.K - c0;
         const int64_t kb = (int64_t)((a.K + 31) >> 5) * 16;
         const uint8_t *codes = a.codes + (it.b * a.M + it.row0) * kb + (c0 >> 1);
-        uint32_t q[4];
+        uint32_t q[4][N / 8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint8_t *src = codes + (int64_t)(32 * i) * kb;
-            q[i] = 0;
-            if (n > 0 && it.row0 + 32 * i < a.M && FP8BQ_IN(FP4_SPAN_C(a), src, 4))
-                asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(q[i]) : "l"(src));
+#pragma unroll
+            for (int j = 0; j < N / 8; ++j) q[i][j] = 0;
+            if (n > 0 && it.row0 + 32 * i < a.M && FP8BQ_IN(FP4_SPAN_C(a), src, N / 2)) {
+                if constexpr (N == 16)
+                    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+                                 : "=r"(q[i][0]), "=r"(q[i][1]) : "l"(src));
+                else
+                    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];"
+                                 : "=r"(q[i][0]) : "l"(src));
+            }
         }
         const int tile = it.seg * (32 / TL) + lane / TL, blk = (lane % TL) / LPB;
         const uint8_t *run =
@@ -436,57 +476,45 @@ __global__ void __launch_bounds__(256) k_fp4_dequant(const __grid_constant__ Fp4
         for (int i = 0; i < 4; ++i) {
             if (it.row0 + 32 * i >= a.M) break;        // the same for the whole warp
             const float s = scale_value<FMT>((sv[i] >> (8 * blk)) & 0xffu);
-            float v[8];
-            decode4(q[i], v[0], v[1], v[2], v[3]);
-            decode4(q[i] >> 16, v[4], v[5], v[6], v[7]);
+            uint32_t o[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                v[j] = __fmul_rn(v[j], s);             // exact
-                if (FMT == FP8BQ_NVFP4) v[j] = __fmul_rn(v[j], t);
+            for (int j = 0; j < N / 4; ++j) {
+                float v[4];
+                decode4(q[i][j / 2] >> (16 * (j & 1)), v[0], v[1], v[2], v[3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] = __fmul_rn(v[e], s);         // exact
+                    if (FMT == FP8BQ_NVFP4) v[e] = __fmul_rn(v[e], t);
+                    if (OES == 4) o[(4 * j + e) & 7] = __float_as_uint(v[e]);
+                }
+                if constexpr (OES == 2) {
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[2 * j]) : "f"(v[1]), "f"(v[0]));
+                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[2 * j + 1]) : "f"(v[3]), "f"(v[2]));
+                }
             }
             char *dst = (char *)const_cast<void *>(a.x) +
                         (it.b * a.xbs + (int64_t)(it.row0 + 32 * i) * a.ld + c0) * OES;
-            uint32_t o[2 * OES];
-#pragma unroll
-            for (int j = 0; j < 2 * OES; ++j) {
-                if constexpr (OES == 2)
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
-                else
-                    o[j] = __float_as_uint(v[j]);
-            }
             if constexpr (kStaged) {
                 char *buf = stage[threadIdx.x >> 5];
-#pragma unroll
-                for (int j = 0; j < OES / 2; ++j)
-                    *(uint4 *)(buf + lane * 8 * OES + 16 * j) =
-                        make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                *(uint4 *)(buf + lane * 32) = make_uint4(o[0], o[1], o[2], o[3]);
+                *(uint4 *)(buf + lane * 32 + 16) = make_uint4(o[4], o[5], o[6], o[7]);
                 __syncwarp();
-                stage_to_row<OES, (ALIGN < 16 ? ALIGN : 16)>(
-                    buf, lane, a.K - it.seg * kFp4ItemCols, dst - lane * 8 * OES, os);
+                stage_to_row<OES, ALIGN>(buf, lane, a.K - it.seg * 32 * N, dst - lane * 32, os);
                 __syncwarp();
-            } else if (n >= 8) {
-                if (!FP8BQ_IN(os, dst, 8 * OES)) continue;
-                if constexpr (OES == 4)
+            } else if (n >= N) {
+                if (FP8BQ_IN(os, dst, 32))
                     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
-                                 "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[2 * OES - 4]),
-                                 "r"(o[2 * OES - 3]), "r"(o[2 * OES - 2]), "r"(o[2 * OES - 1])
+                                 "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]),
+                                 "r"(o[6]), "r"(o[7])
                                  : "memory");
-                else if constexpr (ALIGN >= 16)
-                    asm volatile("st.global.cs.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(dst), "r"(o[0]),
-                                 "r"(o[1]), "r"(o[2]), "r"(o[3])
-                                 : "memory");
-                else
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        *(uint2 *)(dst + 8 * j) = make_uint2(o[2 * j], o[2 * j + 1]);
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < N; ++j)
                     if (j < n && FP8BQ_IN(os, dst + j * OES, OES)) {
                         if constexpr (OES == 2)
                             *(uint16_t *)(dst + 2 * j) = (uint16_t)(o[j / 2] >> (16 * (j & 1)));
                         else
-                            *(uint32_t *)(dst + 4 * j) = o[j % (2 * OES)];
+                            *(uint32_t *)(dst + 4 * j) = o[j];
                     }
             }
         }
@@ -499,13 +527,14 @@ unsigned fp4_grid(uint64_t items, int per_sm) {  // a warp an item, 8 warps a CT
     return (unsigned)(need < 1 ? 1 : need < cap ? need : cap);
 }
 
-#ifndef FP8BQ_FP4_CTAS_PER_SM
-#define FP8BQ_FP4_CTAS_PER_SM 32
-#endif
+// Grid cap.  Measured on B200, 12288 x 4096 bf16 and 65536 x 4096: 16 a SM
+// 2-4 % slower, 64 and more within 1 % either way.
+constexpr int kFp4CtasPerSm = 32;
 
 template <int FMT, int ES, int MAXD>
 cudaError_t quant_align(const Fp4Pack<MAXD> &p, int align, cudaStream_t st) {
-    const unsigned grid = fp4_grid(p.total, FP8BQ_FP4_CTAS_PER_SM);
+    const unsigned grid = fp4_grid(p.total, kFp4CtasPerSm);
+    if (align >= 32) return launch_kernel(k_fp4_quant<FMT, ES, 32, MAXD>, grid, 256, 0, st, p);
     if (align >= 16) return launch_kernel(k_fp4_quant<FMT, ES, 16, MAXD>, grid, 256, 0, st, p);
     if (align >= 8) return launch_kernel(k_fp4_quant<FMT, ES, 8, MAXD>, grid, 256, 0, st, p);
     return launch_kernel(k_fp4_quant<FMT, ES, ES, MAXD>, grid, 256, 0, st, p);
@@ -513,10 +542,8 @@ cudaError_t quant_align(const Fp4Pack<MAXD> &p, int align, cudaStream_t st) {
 
 template <int FMT, int OES, int MAXD>
 cudaError_t dequant_align(const Fp4Pack<MAXD> &p, int align, cudaStream_t st) {
-    const unsigned grid = fp4_grid(p.total, FP8BQ_FP4_CTAS_PER_SM);
-    if constexpr (OES == 4)
-        if (align >= 32)
-            return launch_kernel(k_fp4_dequant<FMT, OES, 32, MAXD>, grid, 256, 0, st, p);
+    const unsigned grid = fp4_grid(p.total, kFp4CtasPerSm);
+    if (align >= 32) return launch_kernel(k_fp4_dequant<FMT, OES, 32, MAXD>, grid, 256, 0, st, p);
     if (align >= 16) return launch_kernel(k_fp4_dequant<FMT, OES, 16, MAXD>, grid, 256, 0, st, p);
     if (align >= 8) return launch_kernel(k_fp4_dequant<FMT, OES, 8, MAXD>, grid, 256, 0, st, p);
     return launch_kernel(k_fp4_dequant<FMT, OES, OES, MAXD>, grid, 256, 0, st, p);
