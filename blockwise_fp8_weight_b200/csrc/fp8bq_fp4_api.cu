@@ -304,6 +304,10 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     const fp8bq_status sd = device_status();
     if (sd != FP8BQ_OK) return sd;
 
+    // the kernels number their tiles in 32 bits
+    if (((__int128)(D.M + 15) / 16) * ((D.N + 127) / 128) * D.batch >= (1ll << 31))
+        return FP8BQ_ERR_SHAPE;
+
     const bool wide = D.M > 256;
     const int tokens = fp4_narrow_tokens(D.M, gated);
     Fp4MmParams p;
@@ -331,7 +335,7 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     p.mma_k = (int32_t)((kb + 31) / 32);
     p.split = 1;
     p.store_align = es;
-    for (int a : {8, 16, 32})
+    for (int a : {4, 8, 16, 32})
         if ((uintptr_t)D.out % a == 0 && D.ld_out * es % a == 0 && obs * es % a == 0)
             p.store_align = a;
     for (int i = 0; i < n; ++i)  // a stack stride of 0: one matrix for the whole stack

@@ -64,22 +64,6 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
     return (uint64_t)((addr & 0x3ffff) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
            (2ull << 61);
 }
-// Descriptor of a 512-byte scale tile: 32 rows of 16 bytes, no swizzle,
-// groups of eight rows 128 bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
-    return (uint64_t)((addr & 0x3ffff) >> 4) | (8ull << 16) | (8ull << 32) | (1ull << 46);
-}
-
-// A scale tile into four tensor-memory columns (row r: lane r % 32 of every
-// quarter, column r / 32, its four blocks in the column's four bytes).
-template <int CG>
-__device__ __forceinline__ void scales_to_tmem(uint32_t dst, uint64_t desc) {
-    if constexpr (CG == 1)
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(dst), "l"(desc));
-    else
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(dst), "l"(desc));
-}
-
 // ---------------------------------------------------------------- block-scaled MMA
 
 // Instruction word: e2m1 operands, fp32 sums, both K-major, tile m x n, e8m0
@@ -185,6 +169,13 @@ __device__ __forceinline__ void tma_load_3d_pair(void *smem_dst, const void *tma
         ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(smem_dst)),
         "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
+}
+// The tile into L2 only: safe before the previous kernel of the stream is
+// done, whose writes go through L2 as well.
+__device__ __forceinline__ void tma_prefetch_3d(const void *tmap, int c0, int c1, int c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(tmap),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
 }
 __device__ __forceinline__ float4 peer_ld4(uint32_t addr) {
     float4 v;

@@ -72,19 +72,37 @@ __device__ __forceinline__ void store4(const Fp4MmParams &p, int64_t e, int64_t 
     }
 }
 
+// Scales of a stage into tensor memory, by one warp for its lane quarter.  A
+// scale tile takes four columns; lane l of column c holds the four blocks of
+// row l + 32 c, so a lane's 16 bytes of a tile are its words of the columns,
+// and every quarter gets the same copy.  The scales go through registers
+// (ld.shared, tcgen05.st) rather than by tcgen05.cp: a copy of one tile holds
+// up the tensor cores for 62 clocks.
+template <int TILES>
+__device__ __forceinline__ void scales_to_tmem(uint32_t dst, const uint4 (&v)[TILES]) {
+    static_assert(TILES % 2 == 0, "pairs of tiles");
+#pragma unroll
+    for (int t = 0; t < TILES; t += 2) dev::tmem_st8(dst + 4 * t, v[t], v[t + 1]);
+    dev::tmem_st_wait();
+}
+
 // ============================================================== few tokens
 //
 // A CTA computes 128 outputs (rows of the weight, the M side of the tensor
 // core's tile) for NT tokens (its N side): few tokens cost few MMA columns,
-// and the kernel is bound by the weight's bytes.  Where the tiles are too few
-// to keep every SM loading, a cluster of `split` CTAs shares a tile: each sums
-// a run of K, the partial sums meet in shared memory, and every CTA of the
-// cluster adds up and stores a part of the tile, in the order of the ranks:
-// no atomics, no workspace, the same sum every time.
+// and the kernel is bound by the weight's bytes.
 //
-// Warp 0 loads (one lane), warp 1 issues the products (one lane), all four
-// warps store.  Every wait is bounded; one that runs out sets the error word,
-// and the CTA still waits for its copies and products before it leaves.
+// Where the tiles are too few to keep every SM loading, a cluster of `split`
+// CTAs shares a tile: each sums a run of K, the partial sums meet in shared
+// memory, and every CTA of the cluster adds up and stores a part of the tile,
+// in the order of the ranks: no atomics, no workspace, the same sum every
+// time.  Otherwise (split == 1) a CTA walks over tiles, and loads and
+// multiplies the next one while it stores.
+//
+// Warp 0 loads (one lane), warp 1 issues the products (one lane), warps 4-7
+// bring the scales into tensor memory, warps 8-11 store.  Every wait is
+// bounded; one that runs out sets the error word, and the CTA still waits for
+// its copies and products before it leaves.
 template <int FMT, bool GATED, int NT>
 struct Narrow {
     static constexpr int W = GATED ? 2 : 1;
@@ -94,200 +112,350 @@ struct Narrow {
     static constexpr int kCodesW = 128 * 128;
     static constexpr int kCodesX = NT * 128;
     static constexpr int kStage = W * (kCodesW + SF) + kCodesX + XT * SF;
-    // two buffers of scale columns after the sums
-    static constexpr int kSfCols = 4 * KT * (W + XT);
-    static constexpr int kNeed = W * NT + 2 * kSfCols;
-    static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
-    static_assert(kNeed <= 512, "tensor memory");
-    // Two CTAs an SM where the sums leave room, else one.  A CTA that takes
-    // c of the 512 tensor-memory columns takes at least c / 512 of the SM's
-    // shared memory, so CTAs that share an SM always find their columns and
-    // none waits for another's while a third waits for it.
+    static constexpr int kTiles = KT * (W + XT);            // scale tiles of a stage
+    static constexpr int kSfCols = 4 * kTiles;
+    // Sums of two tiles where they fit beside two stages' scales.
+    static constexpr int kSums = W * NT;
+    static constexpr int kAcc = 2 * kSums + 2 * kSfCols <= 512 ? 2 : 1;
+    // Two CTAs an SM where their sums and rings leave room, else one.  A CTA
+    // that takes c of the 512 tensor-memory columns takes at least c / 512 of
+    // the SM's shared memory, so CTAs that share an SM always find their
+    // columns and none waits for another's while a third waits for it.
     static constexpr int kSmall = 114688, kLarge = 231424;  // 112 KB, 226 KB
-    static constexpr int kSmem = kCols <= 128 || (kCols == 256 && 2 * kStage + 1024 <= kSmall)
-                                     ? kSmall
-                                     : kLarge;
+    static constexpr bool kTwo =
+        kAcc * kSums + 2 * kSfCols <= 256 && 2 * kStage + 1024 <= kSmall;
+    static constexpr int kCols = kTwo ? 256 : 512;
+    static constexpr int kSmem = kTwo ? kSmall : kLarge;
     static constexpr int kStages = (kSmem - 1024) / kStage;
-    static_assert(kStages >= 2, "ring");
-    static_assert(W * NT * 128 * 4 <= kStages * kStage, "partial sums");
+    static constexpr int kFit = (kCols - kAcc * kSums) / kSfCols;
+    static constexpr int kSfBufs = kFit < kStages ? kFit : kStages;
+    static constexpr int kThreads = 384;
+    static_assert(kStages >= 2 && kSfBufs >= 2, "ring");
+    static_assert(kSums * 128 * 4 <= kStages * kStage, "partial sums");
+};
+
+// The tiles of a CTA (of its cluster), the same for every role; tiles without
+// valid rows are passed over.  The weight's rows run fastest.
+struct NarrowWalk {
+    const Fp4MmParams &p;
+    uint32_t t, step, total, mt, nt;  // fewer than 2^31 tiles (checked on the host)
+    int width, m0, n0, e, valid;
+    __device__ __forceinline__ NarrowWalk(const Fp4MmParams &q, int width_)
+        : p(q), step(gridDim.x / (uint32_t)q.split), width(width_) {
+        t = blockIdx.x / (uint32_t)q.split;
+        mt = (uint32_t)(p.M + width - 1) / (uint32_t)width;
+        nt = (uint32_t)(p.N + 127) / 128;
+        total = mt * nt * (uint32_t)p.batch;
+    }
+    __device__ __forceinline__ void place() {
+        const uint32_t r = t / nt;
+        n0 = (int)(t - r * nt) * 128;
+        e = mt == 1 ? (int)r : (int)(r / mt);
+        m0 = (int)(r - (uint32_t)e * mt) * width;
+    }
+    __device__ __forceinline__ bool next() {
+        for (; t < total; t += step) {
+            place();
+            valid = min(width, valid_rows(p, e) - m0);
+            if (valid > 0) {
+                t += step;
+                return true;
+            }
+        }
+        return false;
+    }
 };
 
 template <int FMT, bool GATED, bool BF16, int NT>
-__global__ void __launch_bounds__(128) k_fp4_narrow(const __grid_constant__ Fp4MmParams p) {
+__global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
+    k_fp4_narrow(const __grid_constant__ Fp4MmParams p) {
     using S = Narrow<FMT, GATED, NT>;
+    constexpr int ES = BF16 ? 2 : 4;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], sums;
+    __shared__ __align__(8) uint64_t full[S::kStages], empty[S::kStages], scaled[S::kSfBufs];
+    __shared__ __align__(8) uint64_t sums[S::kAcc], freed[S::kAcc], done;
     __shared__ uint32_t tmem_at;
     __shared__ volatile int abort_flag;
     uint8_t *ring = raw + ((1024u - (dev::smem_addr(raw) & 1023u)) & 1023u);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)(blockIdx.x % (unsigned)p.split);
-    const int n0 = (int)(blockIdx.x / (unsigned)p.split) * 128;
-    const int m0 = (int)blockIdx.y * NT;
-    const int e = (int)blockIdx.z;
+    const int k0 = (int)((int64_t)p.stages_k * rank / p.split);
+    const int k1 = (int)((int64_t)p.stages_k * (rank + 1) / p.split);
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             dev::mbar_init(&full[s], 1);
             dev::mbar_init(&empty[s], 1);
         }
-        dev::mbar_init(&sums, 1);
+        for (int s = 0; s < S::kSfBufs; ++s) dev::mbar_init(&scaled[s], 4);
+        for (int s = 0; s < S::kAcc; ++s) {
+            dev::mbar_init(&sums[s], 1);
+            dev::mbar_init(&freed[s], 4);
+        }
+        dev::mbar_init(&done, 1);
         abort_flag = 0;
         dev::fence_mbar_init();
-        dev::prefetch_tensormap(&p.w[0]);
         dev::prefetch_tensormap(&p.x);
     }
     if (warp == 1) dev::tmem_alloc<1>(&tmem_at, S::kCols);
+    NarrowWalk w(p, NT);
+    auto at = [&](int map) { return (p.moves >> map) & 1u ? w.e : 0; };
+    if (warp == 2 && lane == 0) {  // the weight's first stages on their way to L2
+        w.place();
+        for (int k = k0; k < k1 && k < k0 + S::kStages; ++k)
+#pragma unroll
+            for (int v = 0; v < S::W; ++v) {
+                dev::tma_prefetch_3d(&p.w[v], k * 128, w.n0, at(2 + 2 * v));
+                dev::tma_prefetch_3d(&p.ws[v], k * (S::SF / 8), w.n0 / 128, at(3 + 2 * v));
+            }
+    }
     dev::tc_fence_before();
     __syncthreads();
     dev::tc_fence_after();
     dev::pdl_launch_dependents();
     dev::pdl_wait();
     const uint32_t tmem = tmem_at;
-    const int valid = min(NT, valid_rows(p, e) - m0);
-    if (valid > 0) {  // the same for every CTA of a cluster
-        const int k0 = (int)((int64_t)p.stages_k * rank / p.split);
-        const int k1 = (int)((int64_t)p.stages_k * (rank + 1) / p.split);
-        if (warp == 0 && lane == 0) {
-            bool dropped = false;
-            auto at = [&](int map) { return (p.moves >> map) & 1u ? e : 0; };
-            int i = 0;
-            for (; k0 + i < k1; ++i) {
-                const int st = i % S::kStages, round = i / S::kStages, k = k0 + i;
+    auto gave_up = [&] {
+        if (!abort_flag) {
+            atomicOr(&g_fp4_error_word, 1u);
+            abort_flag = 1;
+        }
+    };
+    float *part = reinterpret_cast<float *>(ring);  // [weight][token][128 outputs]
+
+    if (warp == 0 && lane == 0) {
+        bool dropped = false, ok = true;
+        int i = 0;  // stages loaded
+        while (ok && w.next()) {
+            for (int k = k0; k < k1; ++k, ++i) {
+                const int st = i % S::kStages, round = i / S::kStages;
                 if (round > 0 && !dev::mbar_wait_bounded(&empty[st], (round - 1) & 1,
                                                          p.wait_limit_ns, &abort_flag)) {
-                    if (!abort_flag) {
-                        atomicOr(&g_fp4_error_word, 1u);
-                        abort_flag = 1;
-                    }
+                    gave_up();
+                    ok = false;
                     break;
                 }
                 dev::mbar_arrive_expect_tx(&full[st], S::kStage);
-                if ((p.inject & FP8BQ_INJECT_DROP_FIRST_LOAD) && i == 0 &&
-                    (blockIdx.x | blockIdx.y | blockIdx.z) == 0) {
+                if ((p.inject & FP8BQ_INJECT_DROP_FIRST_LOAD) && i == 0 && blockIdx.x == 0) {
                     dropped = true;
                     continue;
                 }
                 uint8_t *b = ring + st * S::kStage;
 #pragma unroll
-                for (int w = 0; w < S::W; ++w, b += S::kCodesW)
-                    dev::tma_load_3d(b, &p.w[w], &full[st], k * 128, n0, at(2 + 2 * w), false);
-                dev::tma_load_3d(b, &p.x, &full[st], k * 128, m0, at(0), false);
+                for (int v = 0; v < S::W; ++v, b += S::kCodesW)
+                    dev::tma_load_3d(b, &p.w[v], &full[st], k * 128, w.n0, at(2 + 2 * v), false);
+                dev::tma_load_3d(b, &p.x, &full[st], k * 128, w.m0, at(0), false);
                 b += S::kCodesX;
 #pragma unroll
-                for (int w = 0; w < S::W; ++w, b += S::SF)
-                    dev::tma_load_3d(b, &p.ws[w], &full[st], k * (S::SF / 8), n0 / 128, at(3 + 2 * w),
-                                     false);
+                for (int v = 0; v < S::W; ++v, b += S::SF)
+                    dev::tma_load_3d(b, &p.ws[v], &full[st], k * (S::SF / 8), w.n0 / 128,
+                                     at(3 + 2 * v), false);
 #pragma unroll
                 for (int t = 0; t < S::XT; ++t, b += S::SF)
-                    dev::tma_load_3d(b, &p.xs, &full[st], k * (S::SF / 8), m0 / 128 + t, at(1), false);
+                    dev::tma_load_3d(b, &p.xs, &full[st], k * (S::SF / 8), w.m0 / 128 + t, at(1),
+                                     false);
             }
-            for (int st = 0; st < S::kStages && st < i; ++st) {  // every copy has landed
-                const int fills = (i - st + S::kStages - 1) / S::kStages;
-                if (dropped && st == 0 && fills == 1) continue;
-                if (!dev::mbar_wait_bounded(&full[st], (fills - 1) & 1, kDrainNs, nullptr))
-                    atomicOr(&g_fp4_error_word, 2u);
+        }
+        for (int st = 0; st < S::kStages && st < i; ++st) {  // every copy has landed
+            const int fills = (i - st + S::kStages - 1) / S::kStages;
+            if (dropped && st == 0 && fills == 1) continue;
+            if (!dev::mbar_wait_bounded(&full[st], (fills - 1) & 1, kDrainNs, nullptr))
+                atomicOr(&g_fp4_error_word, 2u);
+        }
+    } else if (warp == 1 && lane == 0) {
+        constexpr uint32_t word = dev::mma_word(FMT, 128, NT);
+        bool ok = true;
+        int i = 0, n = 0;  // stages, tiles
+        for (; ok && w.next(); ++n) {
+            const int acc = n % S::kAcc;
+            if (n >= S::kAcc && !dev::mbar_wait_bounded(&freed[acc], (n / S::kAcc - 1) & 1,
+                                                        p.wait_limit_ns, &abort_flag)) {
+                gave_up();
+                break;
             }
-        } else if (warp == 1 && lane == 0) {
-            constexpr uint32_t word = dev::mma_word(FMT, 128, NT);
-            for (int i = 0; k0 + i < k1; ++i) {
-                const int st = i % S::kStages, k = k0 + i;
+            for (int k = k0; k < k1; ++k, ++i) {
+                const int st = i % S::kStages;
                 if (!dev::mbar_wait_bounded(&full[st], (i / S::kStages) & 1, p.wait_limit_ns,
-                                            &abort_flag)) {
-                    if (!abort_flag) {
-                        atomicOr(&g_fp4_error_word, 1u);
-                        abort_flag = 1;
-                    }
+                                            &abort_flag) ||
+                    !dev::mbar_wait_bounded(&scaled[i % S::kSfBufs], (i / S::kSfBufs) & 1,
+                                            p.wait_limit_ns, &abort_flag)) {
+                    gave_up();
+                    ok = false;
                     break;
                 }
                 dev::tc_fence_after();
-                const uint32_t at = dev::smem_addr(ring + st * S::kStage);
-                const uint32_t sf = at + S::W * S::kCodesW + S::kCodesX;
-                const uint32_t sw = tmem + S::W * NT + (i & 1) * S::kSfCols;
+                const uint32_t b = dev::smem_addr(ring + st * S::kStage);
+                const uint32_t sw =
+                    tmem + S::kAcc * S::kSums + (i % S::kSfBufs) * S::kSfCols;
                 const uint32_t sx = sw + 4 * S::KT * S::W;
-#pragma unroll
-                for (int t = 0; t < S::KT; ++t) {
-#pragma unroll
-                    for (int w = 0; w < S::W; ++w)
-                        dev::scales_to_tmem<1>(sw + 4 * (w * S::KT + t),
-                                               dev::scale_desc(sf + w * S::SF + t * kFp4TileBytes));
-#pragma unroll
-                    for (int x = 0; x < S::XT; ++x)
-                        dev::scales_to_tmem<1>(
-                            sx + 4 * (t * S::XT + x),
-                            dev::scale_desc(sf + (S::W + x) * S::SF + t * kFp4TileBytes));
-                }
-                const uint64_t xd = dev::operand_desc(at + S::W * S::kCodesW);
+                const uint64_t xd = dev::operand_desc(b + S::W * S::kCodesW);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (4 * k + j >= p.mma_k) break;
                     const int t = j * S::KT / 4;
                     const uint32_t wd = dev::mma_word_id(word, FMT == FP8BQ_MXFP4 ? 2 * (j & 1) : 0);
 #pragma unroll
-                    for (int w = 0; w < S::W; ++w)
-                        dev::mma_fp4<FMT, 1>(tmem + w * NT,
-                                             dev::operand_desc(at + w * S::kCodesW) + 2 * j,
-                                             xd + 2 * j, wd, sw + 4 * (w * S::KT + t),
-                                             sx + 4 * t * S::XT, i + j > 0);
+                    for (int v = 0; v < S::W; ++v)
+                        dev::mma_fp4<FMT, 1>(tmem + acc * S::kSums + v * NT,
+                                             dev::operand_desc(b + v * S::kCodesW) + 2 * j,
+                                             xd + 2 * j, wd, sw + 4 * (v * S::KT + t),
+                                             sx + 4 * t * S::XT, k > k0 || j > 0);
                 }
                 dev::mma_commit<1>(&empty[st]);
             }
-            dev::mma_commit<1>(&sums);
+            dev::mma_commit<1>(&sums[acc]);
         }
-        __syncwarp();
-        // The products give up on their own; a little longer, and they are stuck.
-        bool ok = dev::mbar_wait_bounded(&sums, 0, 2 * p.wait_limit_ns + kDrainNs, nullptr);
-        if (!ok && tid == 0) atomicOr(&g_fp4_error_word, 2u);
-        dev::tc_fence_after();
-        // Sums to shared memory (the ring is free: every copy was waited for
-        // and every product is done), [weight][token][128 outputs].
-        float *part = reinterpret_cast<float *>(ring);
+        dev::mma_commit<1>(&done);
+        if (!dev::mbar_wait_bounded(&done, 0, kDrainNs, nullptr)) atomicOr(&g_fp4_error_word, 2u);
+    } else if (warp >= 4 && warp < 8) {
+        const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+        bool ok = true;
+        for (int i = 0; ok && w.next();) {
+            for (int k = k0; k < k1; ++k, ++i) {
+                const int st = i % S::kStages, b = i % S::kSfBufs;
+                bool here = dev::mbar_wait_bounded(&full[st], (i / S::kStages) & 1, p.wait_limit_ns,
+                                                   &abort_flag);
+                const uint8_t *sf =
+                    ring + st * S::kStage + S::W * S::kCodesW + S::kCodesX + lane * 16;
+                uint4 v[S::kTiles];  // of each weight, then tile by tile of the tokens
 #pragma unroll
-        for (int w = 0; w < S::W; ++w) {
+                for (int t = 0; t < S::KT; ++t) {
 #pragma unroll
-            for (int c = 0; c < NT; c += 16) {
-                if (c >= valid) break;
-                uint32_t v[16];
-                dev::tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + w * NT + c, v);
-                dev::tmem_ld_wait();
+                    for (int u = 0; u < S::W; ++u)
+                        v[u * S::KT + t] = *(const uint4 *)(sf + u * S::SF + t * kFp4TileBytes);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    part[(w * NT + c + j) * 128 + tid] = __uint_as_float(v[j]);
+                    for (int x = 0; x < S::XT; ++x)
+                        v[S::W * S::KT + t * S::XT + x] =
+                            *(const uint4 *)(sf + (S::W + x) * S::SF + t * kFp4TileBytes);
+                }
+                if (i >= S::kSfBufs) {  // the products that read this buffer are done
+                    const int o = i - S::kSfBufs;
+                    here = here && dev::mbar_wait_bounded(&empty[o % S::kStages],
+                                                          (o / S::kStages) & 1, p.wait_limit_ns,
+                                                          &abort_flag);
+                }
+                if (!__all_sync(0xffffffffu, here)) {
+                    if (lane == 0) gave_up();
+                    ok = false;
+                    break;
+                }
+                dev::tc_fence_after();
+                scales_to_tmem<S::kTiles>(
+                    tmem + quarter + S::kAcc * S::kSums + b * S::kSfCols, v);
+                dev::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) dev::mbar_arrive(&scaled[b]);
             }
         }
-        dev::tc_fence_before();
-        if (p.split > 1) dev::cluster_sync();
-        else __syncthreads();
-        ok = ok && !abort_flag;
-        const float xt = MM_XT(p, e);
+    } else if (warp >= 8) {
+        const int row = (warp & 3) * 32 + lane;  // of the weight's 128
+        for (int n = 0; w.next(); ++n) {
+            const int acc = n % S::kAcc;
+            const bool here = dev::mbar_wait_bounded(&sums[acc], (n / S::kAcc) & 1,
+                                                     2 * p.wait_limit_ns, &abort_flag);
+            if (!__all_sync(0xffffffffu, here)) {
+                if (lane == 0) gave_up();
+                break;
+            }
+            dev::tc_fence_after();
+            const uint32_t d = tmem + acc * S::kSums + ((uint32_t)((warp & 3) * 32) << 16);
+            if (p.split > 1) {  // the ring is free: every stage was multiplied
+#pragma unroll
+                for (int c = 0; c < S::kSums; c += 16) {
+                    if (c % NT >= w.valid) continue;
+                    uint32_t v[16];
+                    dev::tmem_ld16(d + c, v);
+                    dev::tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) part[(c + j) * 128 + row] = __uint_as_float(v[j]);
+                }
+                continue;
+            }
+            const float xt = MM_XT(p, w.e), alpha = __fmul_rn(xt, MM_WT(p, 0, w.e));
+            const float alpha1 = GATED ? __fmul_rn(xt, MM_WT(p, 1, w.e)) : 0.0f;
+            const int o = w.n0 + row;
+            char *dst = (char *)p.out + (w.e * p.obs + (int64_t)w.m0 * p.ldo + o) * ES;
+#pragma unroll 1
+            for (int c = 0; c < w.valid; c += 16) {
+                uint32_t g[16], u[16];
+                dev::tmem_ld16(d + c, g);
+                if constexpr (GATED) dev::tmem_ld16(d + NT + c, u);
+                dev::tmem_ld_wait();
+                if (c + 16 >= w.valid) {
+                    dev::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) dev::mbar_arrive(&freed[acc]);
+                }
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    v[j] = __uint_as_float(g[j]) * alpha;
+                    if constexpr (GATED) v[j] = silu(v[j]) * (__uint_as_float(u[j]) * alpha1);
+                }
+                if (BF16 && p.store_align >= 4) {
+                    // two tokens at a time: an even lane stores its and its
+                    // neighbour's output of the first, an odd one of the second
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        const bool odd = lane & 1;
+                        const float get =
+                            __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+                        const uint32_t two = odd ? bf16x2(get, v[j + 1]) : bf16x2(v[j], get);
+                        const int t = c + j + odd;
+                        char *q = dst + (t * p.ldo - odd) * ES;
+                        if (t < w.valid && (o | 1) < p.N) {
+                            if (FP8BQ_IN(MM_SPAN(p.out, p.out_bytes), q, 4)) *(uint32_t *)q = two;
+                        } else if (t < w.valid && (o & ~1) < p.N &&
+                                   FP8BQ_IN(MM_SPAN(p.out, p.out_bytes), q, 2)) {
+                            *(uint16_t *)q = (uint16_t)two;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        char *q = dst + (c + j) * p.ldo * ES;
+                        if (c + j < w.valid && o < p.N &&
+                            FP8BQ_IN(MM_SPAN(p.out, p.out_bytes), q, ES)) {
+                            if constexpr (BF16) *(uint16_t *)q = (uint16_t)bf16x2(v[j], 0.0f);
+                            else *(float *)q = v[j];
+                        }
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
+    dev::tc_fence_before();
+    NarrowWalk one(p, NT);
+    if (p.split > 1 && one.next()) {  // the same for every CTA of a cluster
+        dev::cluster_sync();
+        const float xt = MM_XT(p, one.e);
         float alpha[S::W];
 #pragma unroll
-        for (int w = 0; w < S::W; ++w) alpha[w] = __fmul_rn(xt, MM_WT(p, w, e));
-        const uint32_t at = dev::smem_addr(part);
-        for (int q = rank * 128 + tid; ok && q < valid * 32; q += p.split * 128) {
-            const int t = q >> 5, n = n0 + (q & 31) * 4;
-            if (n >= p.N) continue;
+        for (int v = 0; v < S::W; ++v) alpha[v] = __fmul_rn(xt, MM_WT(p, v, one.e));
+        const uint32_t base = dev::smem_addr(part);
+        for (int q = rank * S::kThreads + tid; !abort_flag && q < one.valid * 32;
+             q += p.split * S::kThreads) {
+            const int t = q >> 5, o = one.n0 + (q & 31) * 4;
+            if (o >= p.N) continue;
             float v[S::W][4];
 #pragma unroll
-            for (int w = 0; w < S::W; ++w) {
-                const uint32_t a = at + ((w * NT + t) * 128 + (q & 31) * 4) * 4;
+            for (int u = 0; u < S::W; ++u) {
+                const uint32_t a = base + ((u * NT + t) * 128 + (q & 31) * 4) * 4;
                 float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
                 for (int r = 0; r < p.split; ++r) {
-                    const float4 o = p.split > 1
-                                         ? dev::peer_ld4(dev::peer_addr(a, r))
-                                         : *reinterpret_cast<const float4 *>(
-                                               part + (w * NT + t) * 128 + (q & 31) * 4);
-                    s.x += o.x, s.y += o.y, s.z += o.z, s.w += o.w;
+                    const float4 f = dev::peer_ld4(dev::peer_addr(a, r));
+                    s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
                 }
-                v[w][0] = s.x * alpha[w], v[w][1] = s.y * alpha[w];
-                v[w][2] = s.z * alpha[w], v[w][3] = s.w * alpha[w];
+                v[u][0] = s.x * alpha[u], v[u][1] = s.y * alpha[u];
+                v[u][2] = s.z * alpha[u], v[u][3] = s.w * alpha[u];
             }
             if constexpr (GATED)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[0][j] = silu(v[0][j]) * v[S::W - 1][j];
-            store4<BF16>(p, e, m0 + t, n, v[0]);
+            store4<BF16>(p, one.e, one.m0 + t, o, v[0]);
         }
-        if (p.split > 1) dev::cluster_sync();  // peers may still read this CTA's sums
+        dev::cluster_sync();  // peers may still read this CTA's sums
     }
     __syncthreads();
     if (warp == 1) dev::tmem_dealloc<1>(tmem, S::kCols);
@@ -310,11 +478,9 @@ __global__ void __launch_bounds__(128) k_fp4_narrow(const __grid_constant__ Fp4M
 // first, and the next tile waits for those alone.  The scales' buffers take
 // the last 96 columns.
 //
-// The scales go through registers (ld.shared, tcgen05.st) rather than by
-// tcgen05.cp: a copy of one scale tile holds up the tensor cores for 62
-// clocks, and a stage has 6 (mxfp4) or 12 (nvfp4) of them beside 768 clocks of
-// products.  Measured on B200, 8192 tokens against 6144 x 16384: clocks a
-// stage 1240 / 1570 with the copies.
+// Measured on B200, 8192 tokens against 6144 x 4096 (mxfp4 / nvfp4): 107 / 110 us;
+// with the scales copied by tcgen05.cp, 6 or 12 tiles a stage beside 768
+// clocks of products: 133 / 171.
 template <int FMT>
 struct Wide {
     static constexpr int KT = 256 / (4 * fp4_block(FMT));
@@ -373,23 +539,25 @@ __device__ __forceinline__ void store32(const Fp4MmParams &p, int64_t e, int64_t
 // the same order for every role; tiles without valid rows are passed over.
 struct WideWalk {
     const Fp4MmParams &p;
-    int64_t t, step, total;
-    int mt, nt, width;
-    int m0, n0, e, valid;
+    uint32_t t, step, total, mt, nt;  // fewer than 2^31 tiles (checked on the host)
+    int width, m0, n0, e, valid;
     __device__ __forceinline__ WideWalk(const Fp4MmParams &q, int width_)
-        : p(q), t((int64_t)(blockIdx.x >> 1) - (gridDim.x >> 1)), step(gridDim.x >> 1), width(width_) {
-        mt = (p.M + 255) / 256;
-        nt = (p.N + width - 1) / width;
-        total = (int64_t)mt * nt * p.batch;
+        : p(q), t(blockIdx.x >> 1), step(gridDim.x >> 1), width(width_) {
+        mt = (uint32_t)(p.M + 255) / 256;
+        nt = (uint32_t)(p.N + width - 1) / (uint32_t)width;
+        total = mt * nt * (uint32_t)p.batch;
     }
     __device__ __forceinline__ bool next() {
-        while ((t += step) < total) {
-            const int64_t r = t / mt;
+        for (; t < total; t += step) {
+            const uint32_t r = t / mt;
             e = (int)(r / nt);
             m0 = (int)(t - r * mt) * 256;
-            n0 = (int)(r - (int64_t)e * nt) * width;
+            n0 = (int)(r - (uint32_t)e * nt) * width;
             valid = valid_rows(p, e);
-            if (m0 < valid) return true;
+            if (m0 < valid) {
+                t += step;
+                return true;
+            }
         }
         return false;
     }
@@ -528,9 +696,6 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
         dev::mma_commit_pair_here(&done);
         if (!dev::mbar_wait_bounded(&done, 0, kDrainNs, nullptr)) atomicOr(&g_fp4_error_word, 2u);
     } else if (warp >= 4 && warp < 8) {
-        // Every lane quarter gets the same copy of the scales: lane l of column
-        // c holds the four blocks of row l + 32 c, so a lane's 16 bytes of a
-        // tile are its words of four columns.
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
         bool ok = true;
         for (int i = 0; ok && w.next();) {
@@ -558,10 +723,7 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
                     break;
                 }
                 dev::tc_fence_after();
-#pragma unroll
-                for (int t = 0; t < 3 * S::KT; t += 2)
-                    dev::tmem_st8(tmem + quarter + S::kScales + b * S::kSfCols + 4 * t, v[t], v[t + 1]);
-                dev::tmem_st_wait();
+                scales_to_tmem<3 * S::KT>(tmem + quarter + S::kScales + b * S::kSfCols, v);
                 dev::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) dev::peer_arrive(dev::peer_addr(dev::smem_addr(&scaled[b]), 0));
@@ -627,7 +789,11 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
 
 template <typename K>
 cudaError_t set_smem(K kernel, int smem) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                cudaSharedmemCarveoutMaxShared);
 }
 
 template <typename K>
@@ -649,23 +815,55 @@ cudaError_t launch_clusters(K kern, dim3 grid, unsigned threads, unsigned cluste
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// Clusters of each size that fit on the device at once (cluster sizes the
+// device cannot run count as 0).
+struct ClusterFit {
+    cudaError_t attr = cudaSuccess;
+    int n[9] = {};
+};
+
+// The occupancy calls count one CTA an SM for any kernel that allocates tensor
+// memory; `per_sm` CTAs are resident (1187 tiles of 128 outputs, one token, K
+// = 4096: 56.5 us with 296 persistent CTAs, 75.5 with 148).
+template <typename K>
+ClusterFit cluster_fit(K kern, unsigned threads, int smem, int per_sm) {
+    ClusterFit f;
+    f.attr = set_smem(kern, smem);
+    for (unsigned c = 1; f.attr == cudaSuccess && c <= 8; ++c) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = 8 * c;
+        cfg.blockDim = threads;
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = c;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        f.attr = cudaOccupancyMaxActiveClusters(&f.n[c], kern, &cfg);
+        f.n[c] *= per_sm;
+    }
+    if (f.attr == cudaSuccess && f.n[1] < 1) f.attr = cudaErrorInvalidConfiguration;
+    return f;
+}
+
 template <int FMT, bool GATED, bool BF16, int NT>
 cudaError_t narrow(const Fp4MmParams &p0, cudaStream_t st) {
     using S = Narrow<FMT, GATED, NT>;
     auto kern = k_fp4_narrow<FMT, GATED, BF16, NT>;
-    static PerDevice<cudaError_t> setup;
-    const cudaError_t e = setup.get([&] { return set_smem(kern, S::kSmem); });
-    if (e != cudaSuccess) return e;
+    static PerDevice<ClusterFit> setup;
+    const ClusterFit fit = setup.get([&] { return cluster_fit(kern, S::kThreads, S::kSmem, S::kTwo ? 2 : 1); });
+    if (fit.attr != cudaSuccess) return fit.attr;
     Fp4MmParams p = p0;
-    const int64_t nt = (p.N + 127) / 128, mt = (p.M + NT - 1) / NT;
-    const int64_t tiles = nt * mt * p.batch;
-    // CTAs that fit at once, shared out over the tiles: the cluster's size
-    const int64_t slots = (int64_t)sm_count() * (S::kSmem == S::kSmall ? 2 : 1);
-    int64_t split = slots / tiles;
-    split = split < 1 ? 1 : split > 8 ? 8 : split;
-    p.split = (int32_t)(split > p.stages_k ? p.stages_k : split);
-    return launch_clusters(kern, dim3((unsigned)(nt * p.split), (unsigned)mt, (unsigned)p.batch),
-                           128, (unsigned)p.split, S::kSmem, st, p);
+    const int64_t tiles = (int64_t)((p.N + 127) / 128) * ((p.M + NT - 1) / NT) * p.batch;
+    // The largest of these cluster sizes with which every tile runs at once
+    // and each CTA has a stage; 5 and 7 measured no better than 4 and 6.
+    p.split = 1;
+    for (int c : {2, 3, 4, 6, 8})
+        if (tiles <= fit.n[c] && c <= p.stages_k) p.split = c;
+    const int64_t clusters = p.split > 1 || tiles < fit.n[1] ? tiles : fit.n[1];
+    return launch_clusters(kern, dim3((unsigned)(clusters * p.split)), S::kThreads,
+                           (unsigned)p.split, S::kSmem, st, p);
 }
 
 template <int FMT, bool GATED, bool BF16>
