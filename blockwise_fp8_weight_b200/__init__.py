@@ -620,11 +620,13 @@ def _fp4_format(format: str) -> tuple[int, int]:
 
 
 def _fp4_setup(tensor, what: str):
-    """(torch, current device, its current stream) of a call on ``tensor``."""
+    """(torch, current device, its current stream, the library) of a call on ``tensor``."""
     import torch
-    _check_cuda(tensor, what)
-    dev = tensor.get_device()
-    return torch, dev, torch._C._cuda_getCurrentRawStream(dev)
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    if not isinstance(tensor, torch.Tensor) or tensor.get_device() != dev:
+        _check_cuda(tensor, what)
+        dev = tensor.get_device()
+    return torch, dev, torch._C._cuda_getCurrentRawStream(dev), _lib or lib()
 
 
 def _fp4_empty(shape, dtype, like, stream):
@@ -687,11 +689,11 @@ def scaled_fp4_blockwise(data_hp, format="mxfp4", tensor_scale=None, stream=None
     gives them row by row).  Both are padded with zeros.
     """
     _, block = _fp4_format(format)
-    torch, _, current = _fp4_setup(data_hp, "data_hp")
+    torch, _, current, L = _fp4_setup(data_hp, "data_hp")
     cs, ss, rec = _fp4_record(data_hp, "data_hp", format, block, tensor_scale)
     codes = _fp4_empty(cs, torch.uint8, data_hp, stream)
     scales = _fp4_empty(ss, torch.uint8, data_hp, stream)
-    st = lib().fp8bq_fp4_quantize_batched(
+    st = L.fp8bq_fp4_quantize_batched(
         _FP4_DESC.pack(data_hp.data_ptr(), codes.data_ptr(), scales.data_ptr(), *rec), 1,
         current if stream is None else _stream(stream))
     if st:
@@ -746,22 +748,25 @@ def quant_weights_fp4(weights: Iterable, format="mxfp4", stream=None):
 
 def _fp4_operand(torch, dev, codes, scales, tensor_scale, format: str, block: int, what: str):
     """The fields of an ``fp8bq_fp4_operand``, then its batch (0 for a plain
-    matrix), rows and bytes a row."""
+    matrix), rows, bytes a row and dimensions."""
     if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor) and
             codes.get_device() == scales.get_device() == dev):
         _check_cuda(codes, what)
         _check_cuda(scales, f"{what}'s scales")
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
         raise TypeError(f"{what}: codes and scales must be uint8")
     shape, ss = codes.shape, scales.shape
-    dim = len(shape)
-    if dim not in (2, 3) or len(ss) != dim + 2:
+    dim, E, Es = len(shape), 0, 0
+    try:
+        if dim == 2:
+            (rows, kb), (mt, kt, r, c) = shape, ss
+        else:
+            (E, rows, kb), (Es, mt, kt, r, c) = shape, ss
+    except ValueError:
         raise ValueError(f"{what}: expected codes [(E,) M, K / 2] and scales "
-                         "[(E,) M tiles, K tiles, 32, 16]")
-    E = shape[0] if dim == 3 else 0
-    rows, kb = shape[-2], shape[-1]
-    mt, kt = -(-rows // 128), -(-kb // (2 * block))
-    if kb % 16 or ss[-4:] != (mt, kt, 32, 16) or (dim == 3 and ss[0] != E):
+                         "[(E,) M tiles, K tiles, 32, 16]") from None
+    if kb & 15 or E != Es or r != 32 or c != 16 or mt != (rows + 127) // 128 or \
+            kt != (kb + 2 * block - 1) // (2 * block):
         raise ValueError(f"{what}: codes {tuple(shape)} do not go with {format} scales {tuple(ss)}")
     if codes.is_contiguous() and scales.is_contiguous():
         cbs, sbs = rows * kb, mt * kt * 512
@@ -783,7 +788,7 @@ def dequantize_fp4_blockwise(codes, scales, format="mxfp4", columns=None, tensor
     """Reverse map of ``scaled_fp4_blockwise``: the values as bf16 (default) or
     fp32, [(E,) M, columns] (default: every column the codes have room for)."""
     fmt, block = _fp4_format(format)
-    torch, dev, current = _fp4_setup(codes, "codes")
+    torch, dev, current, L = _fp4_setup(codes, "codes")
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out_dtype must be torch.bfloat16 or torch.float32")
@@ -795,7 +800,7 @@ def dequantize_fp4_blockwise(codes, scales, format="mxfp4", columns=None, tensor
     if E > 1 and (cbs != M * kb or sbs != scales[0].numel()):
         raise ValueError("a stack's codes and scales must be contiguous")
     out = _fp4_empty((M, K) if dim == 2 else (E, M, K), out_dtype, codes, stream)
-    st = lib().fp8bq_fp4_dequantize(c, s, E if dim == 3 else 1, M, K, fmt, t, ts, out.data_ptr(),
+    st = L.fp8bq_fp4_dequantize(c, s, E if dim == 3 else 1, M, K, fmt, t, ts, out.data_ptr(),
                                     FP8BQ_BF16 if out_dtype == torch.bfloat16 else FP8BQ_F32, K,
                                     M * K, current if stream is None else _stream(stream))
     if st:
@@ -803,9 +808,9 @@ def dequantize_fp4_blockwise(codes, scales, format="mxfp4", columns=None, tensor
     return out
 
 
-def _fp4_product(entry, a, b, up, format, out_dtype, rows, out, stream, what):
+def _fp4_product(what, a, b, up, format, out_dtype, rows, out, stream):
     fmt, block = _fp4_format(format)
-    torch, dev, current = _fp4_setup(a[0], "a")
+    torch, dev, current, L = _fp4_setup(a[0], "a")
     *fa, E, M, kb, dim = _fp4_operand(torch, dev, *a, format, block, "a")
     *fb, Eb, N, kb_b, dim_b = _fp4_operand(torch, dev, *b, format, block,
                                            "b" if up is None else "gate")
@@ -841,13 +846,13 @@ def _fp4_product(entry, a, b, up, format, out_dtype, rows, out, stream, what):
         if N > 1 and st[-1] != 1:
             raise ValueError("the last dimension of out must have unit stride")
         ld, obs = (max(st[-2], N) if M > 1 else N), (st[0] if dim == 3 else 0)
-    st = entry(_FP4_MATMUL_DESC.pack(
+    st = getattr(L, "fp8bq_fp4_" + what)(_FP4_MATMUL_DESC.pack(
         *fa, *fb, *fu, out.data_ptr(), 0 if rows is None else rows.data_ptr(), M, N, 2 * kb,
         E if dim == 3 else 1, ld, obs, fmt,
         FP8BQ_BF16 if out_dtype == torch.bfloat16 else _dtype_code(out)),
         current if stream is None else _stream(stream))
     if st:
-        check(st, what)
+        check(st, what + "_fp4")
     return out
 
 
@@ -863,9 +868,8 @@ def matmul_fp4(a, a_scales, b, b_scales, format="mxfp4", a_tensor_scale=None, b_
 
     The codes carry no gradient: they are what an inference engine holds.
     """
-    return _fp4_product(lib().fp8bq_fp4_matmul, (a, a_scales, a_tensor_scale),
-                        (b, b_scales, b_tensor_scale), None, format, out_dtype, rows, out, stream,
-                        "matmul_fp4")
+    return _fp4_product("matmul", (a, a_scales, a_tensor_scale), (b, b_scales, b_tensor_scale),
+                        None, format, out_dtype, rows, out, stream)
 
 
 def gated_matmul_fp4(a, a_scales, gate, gate_scales, up, up_scales, format="mxfp4",
@@ -875,6 +879,6 @@ def gated_matmul_fp4(a, a_scales, gate, gate_scales, up, up_scales, format="mxfp
     kernel; operands and arguments as in ``matmul_fp4``.  The halves of a fused
     [(E,) 2F, K] weight may be views of it where F is a multiple of 128
     (codes[..., :F, :], scales[..., :F // 128, :, :, :], and the rest)."""
-    return _fp4_product(lib().fp8bq_fp4_gated_matmul, (a, a_scales, a_tensor_scale),
+    return _fp4_product("gated_matmul", (a, a_scales, a_tensor_scale),
                         (gate, gate_scales, gate_tensor_scale), (up, up_scales, up_tensor_scale),
-                        format, out_dtype, rows, out, stream, "gated_matmul_fp4")
+                        format, out_dtype, rows, out, stream)

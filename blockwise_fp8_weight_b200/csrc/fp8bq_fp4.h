@@ -17,6 +17,13 @@ uint32_t inject_flags();            // FP8BQ_INJECT_*
 uint64_t checked_extent(uint64_t);  // an output's extent for the bounds checks
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
+// Whether a call of this much work is launched with programmatic stream
+// serialization.  The attribute costs the host 1.6 us a launch (4.2 against
+// 2.6 on the pool's hosts), more than the overlap saves where the host is the
+// slower side: calls that take the device less than a few microseconds,
+// outside a graph.
+bool fp4_overlap(cudaStream_t st, double bytes, double flops);
+
 // ------------------------------------------------------------------ layout
 //
 // Codes: rows of 16 * ceil(K / 32) bytes.  Scales: tiles of 128 rows by four
@@ -68,10 +75,10 @@ static_assert(sizeof(Fp4Pack<kMaxFp4Large>) < 32000, "kernel parameter limit");
 // allows (32, 16, 8 or the element's size)
 template <int MAXD>
 cudaError_t launch_fp4_quantize(const Fp4Pack<MAXD> &p, int format, int esize, int align,
-                                cudaStream_t st);
+                                bool overlap, cudaStream_t st);
 template <int MAXD>
 cudaError_t launch_fp4_dequantize(const Fp4Pack<MAXD> &p, int format, int esize, int align,
-                                  cudaStream_t st);
+                                  bool overlap, cudaStream_t st);
 
 // ------------------------------------------------------------------ products
 
@@ -87,6 +94,7 @@ struct Fp4MmParams {
     int32_t M, N, batch;
     int32_t stages_k;  // ceil(K / 256)
     int32_t mma_k;     // ceil(K / 64)
+    int32_t overlap;   // launch with programmatic stream serialization (host)
     int32_t split;     // CTAs that share a tile's K range (a cluster)
     int32_t store_align; // bytes (32, 16, 8 or the element's) that every output row is aligned to
     uint32_t moves;    // bit i: operand map i steps with the stack (x, xs, w[0], ws[0], w[1], ws[1])

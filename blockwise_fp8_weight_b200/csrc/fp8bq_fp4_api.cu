@@ -10,6 +10,17 @@
 
 using namespace fp8bq;
 
+bool fp8bq::fp4_overlap(cudaStream_t st, double bytes, double flops) {
+    if (!pdl_enabled()) return false;
+    if (bytes / 6.5e12 + flops / 3.5e15 > 8e-6) return true;
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return cs != cudaStreamCaptureStatusNone;
+}
+
 namespace {
 
 constexpr int64_t kMaxDim = (1ll << 31) - 256;
@@ -119,7 +130,7 @@ int align_of(const Stack &D) {
 
 template <int MAXD>
 cudaError_t quantize_group(const std::vector<Stack> &t, const std::vector<int> &idx, int align,
-                           cudaStream_t st) {
+                           bool overlap, cudaStream_t st) {
     static thread_local Fp4Pack<MAXD> p;  // large: keep it off the stack
     const Stack &first = t[idx[0]];
     for (size_t i = 0; i < idx.size();) {
@@ -130,7 +141,7 @@ cudaError_t quantize_group(const std::vector<Stack> &t, const std::vector<int> &
             p.total += p.d[p.n].items;
         }
         const cudaError_t e =
-            launch_fp4_quantize<MAXD>(p, first.format, esize_of(first.dtype), align, st);
+            launch_fp4_quantize<MAXD>(p, first.format, esize_of(first.dtype), align, overlap, st);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -141,12 +152,14 @@ fp8bq_status run_quantize(std::vector<Stack> &t, cudaStream_t stream) {
     std::vector<int> groups[2][2][4];  // format, fp32 input, alignment
     static constexpr int kAligns[4] = {32, 16, 8, 0};
     bool any = false;
+    double bytes = 0;
     for (size_t i = 0; i < t.size(); ++i) {
         bool empty = false;
         const fp8bq_status s = check_stack(t[i], false, &empty);
         if (s != FP8BQ_OK) return s;
         if (empty) continue;
         any = true;
+        bytes += (double)t[i].batch * t[i].M * t[i].K * (esize_of(t[i].dtype) + 0.5);
         add_range(ranges, t[i].x, t[i].x_bytes(), false);
         add_range(ranges, t[i].codes, t[i].code_bytes(), true);
         add_range(ranges, t[i].scales, t[i].scale_bytes(), true);
@@ -158,14 +171,16 @@ fp8bq_status run_quantize(std::vector<Stack> &t, cudaStream_t stream) {
     if (overlaps(ranges)) return FP8BQ_ERR_OVERLAP;
     const fp8bq_status sd = device_status();
     if (sd != FP8BQ_OK) return sd;
+    const bool overlap = fp4_overlap(stream, bytes, 0);
     for (auto &by_format : groups)
         for (auto &by_type : by_format)
             for (int a = 0; a < 4; ++a) {
                 const std::vector<int> &g = by_type[a];
                 if (g.empty()) continue;
-                const cudaError_t e = g.size() <= (size_t)kMaxDescSmall
-                                          ? quantize_group<kMaxDescSmall>(t, g, kAligns[a], stream)
-                                          : quantize_group<kMaxFp4Large>(t, g, kAligns[a], stream);
+                const cudaError_t e =
+                    g.size() <= (size_t)kMaxDescSmall
+                        ? quantize_group<kMaxDescSmall>(t, g, kAligns[a], overlap, stream)
+                        : quantize_group<kMaxFp4Large>(t, g, kAligns[a], overlap, stream);
                 if (e != cudaSuccess) {
                     cudaGetLastError();
                     return FP8BQ_ERR_DEVICE;
@@ -196,7 +211,9 @@ fp8bq_status run_dequantize(Stack D, cudaStream_t stream) {
     p.n = 1;
     fill(D, true, 0, &p.d[0]);
     p.total = p.d[0].items;
-    if (launch_fp4_dequantize<kMaxDescSmall>(p, D.format, esize_of(D.dtype), align_of(D), stream) !=
+    const int es = esize_of(D.dtype);
+    const bool overlap = fp4_overlap(stream, (double)D.batch * D.M * D.K * (es + 0.5), 0);
+    if (launch_fp4_dequantize<kMaxDescSmall>(p, D.format, es, align_of(D), overlap, stream) !=
         cudaSuccess) {
         cudaGetLastError();
         return FP8BQ_ERR_DEVICE;
@@ -340,6 +357,8 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
             p.store_align = a;
     for (int i = 0; i < n; ++i)  // a stack stride of 0: one matrix for the whole stack
         p.moves |= (mats[i].cbs ? 1u : 0u) << (2 * i) | (mats[i].sbs ? 2u : 0u) << (2 * i);
+    const double weights = (double)(n - 1) * D.batch * D.N * D.K;
+    p.overlap = fp4_overlap(stream, 0.5 * weights + (double)out_bytes, 2.0 * weights * D.M);
     p.inject = inject_flags();
 #if FP8BQ_CHECKED
     p.out_bytes = checked_extent((uint64_t)out_bytes);

@@ -531,52 +531,66 @@ unsigned fp4_grid(uint64_t items, int per_sm) {  // a warp an item, 8 warps a CT
 // 2-4 % slower, 64 and more within 1 % either way.
 constexpr int kFp4CtasPerSm = 32;
 
+template <typename K, typename P>
+cudaError_t launch_fp4(bool overlap, K kern, unsigned grid, cudaStream_t st, const P &p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = 256;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 template <int FMT, int ES, int MAXD>
-cudaError_t quant_align(const Fp4Pack<MAXD> &p, int align, cudaStream_t st) {
+cudaError_t quant_align(const Fp4Pack<MAXD> &p, int align, bool overlap, cudaStream_t st) {
     const unsigned grid = fp4_grid(p.total, kFp4CtasPerSm);
-    if (align >= 32) return launch_kernel(k_fp4_quant<FMT, ES, 32, MAXD>, grid, 256, 0, st, p);
-    if (align >= 16) return launch_kernel(k_fp4_quant<FMT, ES, 16, MAXD>, grid, 256, 0, st, p);
-    if (align >= 8) return launch_kernel(k_fp4_quant<FMT, ES, 8, MAXD>, grid, 256, 0, st, p);
-    return launch_kernel(k_fp4_quant<FMT, ES, ES, MAXD>, grid, 256, 0, st, p);
+    if (align >= 32) return launch_fp4(overlap, k_fp4_quant<FMT, ES, 32, MAXD>, grid, st, p);
+    if (align >= 16) return launch_fp4(overlap, k_fp4_quant<FMT, ES, 16, MAXD>, grid, st, p);
+    if (align >= 8) return launch_fp4(overlap, k_fp4_quant<FMT, ES, 8, MAXD>, grid, st, p);
+    return launch_fp4(overlap, k_fp4_quant<FMT, ES, ES, MAXD>, grid, st, p);
 }
 
 template <int FMT, int OES, int MAXD>
-cudaError_t dequant_align(const Fp4Pack<MAXD> &p, int align, cudaStream_t st) {
+cudaError_t dequant_align(const Fp4Pack<MAXD> &p, int align, bool overlap, cudaStream_t st) {
     const unsigned grid = fp4_grid(p.total, kFp4CtasPerSm);
-    if (align >= 32) return launch_kernel(k_fp4_dequant<FMT, OES, 32, MAXD>, grid, 256, 0, st, p);
-    if (align >= 16) return launch_kernel(k_fp4_dequant<FMT, OES, 16, MAXD>, grid, 256, 0, st, p);
-    if (align >= 8) return launch_kernel(k_fp4_dequant<FMT, OES, 8, MAXD>, grid, 256, 0, st, p);
-    return launch_kernel(k_fp4_dequant<FMT, OES, OES, MAXD>, grid, 256, 0, st, p);
+    if (align >= 32) return launch_fp4(overlap, k_fp4_dequant<FMT, OES, 32, MAXD>, grid, st, p);
+    if (align >= 16) return launch_fp4(overlap, k_fp4_dequant<FMT, OES, 16, MAXD>, grid, st, p);
+    if (align >= 8) return launch_fp4(overlap, k_fp4_dequant<FMT, OES, 8, MAXD>, grid, st, p);
+    return launch_fp4(overlap, k_fp4_dequant<FMT, OES, OES, MAXD>, grid, st, p);
 }
 
 }  // namespace
 
 template <int MAXD>
 cudaError_t launch_fp4_quantize(const Fp4Pack<MAXD> &p, int format, int esize, int align,
-                                cudaStream_t st) {
+                                bool overlap, cudaStream_t st) {
     if (format == FP8BQ_MXFP4)
-        return esize == 2 ? quant_align<FP8BQ_MXFP4, 2>(p, align, st)
-                          : quant_align<FP8BQ_MXFP4, 4>(p, align, st);
-    return esize == 2 ? quant_align<FP8BQ_NVFP4, 2>(p, align, st)
-                      : quant_align<FP8BQ_NVFP4, 4>(p, align, st);
+        return esize == 2 ? quant_align<FP8BQ_MXFP4, 2>(p, align, overlap, st)
+                          : quant_align<FP8BQ_MXFP4, 4>(p, align, overlap, st);
+    return esize == 2 ? quant_align<FP8BQ_NVFP4, 2>(p, align, overlap, st)
+                      : quant_align<FP8BQ_NVFP4, 4>(p, align, overlap, st);
 }
 
 template <int MAXD>
 cudaError_t launch_fp4_dequantize(const Fp4Pack<MAXD> &p, int format, int esize, int align,
-                                  cudaStream_t st) {
+                                  bool overlap, cudaStream_t st) {
     if (format == FP8BQ_MXFP4)
-        return esize == 2 ? dequant_align<FP8BQ_MXFP4, 2>(p, align, st)
-                          : dequant_align<FP8BQ_MXFP4, 4>(p, align, st);
-    return esize == 2 ? dequant_align<FP8BQ_NVFP4, 2>(p, align, st)
-                      : dequant_align<FP8BQ_NVFP4, 4>(p, align, st);
+        return esize == 2 ? dequant_align<FP8BQ_MXFP4, 2>(p, align, overlap, st)
+                          : dequant_align<FP8BQ_MXFP4, 4>(p, align, overlap, st);
+    return esize == 2 ? dequant_align<FP8BQ_NVFP4, 2>(p, align, overlap, st)
+                      : dequant_align<FP8BQ_NVFP4, 4>(p, align, overlap, st);
 }
 
 template cudaError_t launch_fp4_quantize<kMaxDescSmall>(const Fp4Pack<kMaxDescSmall> &, int, int,
-                                                        int, cudaStream_t);
+                                                        int, bool, cudaStream_t);
 template cudaError_t launch_fp4_quantize<kMaxFp4Large>(const Fp4Pack<kMaxFp4Large> &, int, int, int,
-                                                       cudaStream_t);
+                                                       bool, cudaStream_t);
 template cudaError_t launch_fp4_dequantize<kMaxDescSmall>(const Fp4Pack<kMaxDescSmall> &, int, int,
-                                                          int, cudaStream_t);
+                                                          int, bool, cudaStream_t);
 
 FP8BQ_DEFINE_BOUNDS_RECORD(bounds_record_fp4_quant)
 
