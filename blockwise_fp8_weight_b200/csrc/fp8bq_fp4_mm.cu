@@ -46,6 +46,19 @@ __device__ __forceinline__ float tensor_scale(const float *t, int64_t stride, in
 #define MM_WT(p, i, e) tensor_scale((p).wt[i], (p).wtbs[i], e, 0)
 #endif
 
+// A place in a ring of N slots and the parity of its round.
+template <int N>
+struct Slot {
+    int at = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) {
+            at = 0;
+            parity ^= 1;
+        }
+    }
+};
+
 // Valid rows of matrix e.
 __device__ __forceinline__ int valid_rows(const Fp4MmParams &p, int e) {
     if (p.rows == nullptr || !FP8BQ_IN(MM_SPAN(p.rows, p.rows_bytes), p.rows + e, 4)) return p.M;
@@ -140,22 +153,36 @@ struct NarrowWalk {
     const Fp4MmParams &p;
     uint32_t t, step, total, mt, nt;  // fewer than 2^31 tiles (checked on the host)
     int width, m0, n0, e, valid;
+    bool placed;  // (m0, n0, e) is tile t's
+    // The first tile's place is found here, ahead of the wait for the previous
+    // kernel: `rows` may be what that kernel writes, and is read by next().
     __device__ __forceinline__ NarrowWalk(const Fp4MmParams &q, int width_)
-        : p(q), step(gridDim.x / (uint32_t)q.split), width(width_) {
-        t = blockIdx.x / (uint32_t)q.split;
+        : p(q), step(gridDim.x), width(width_), placed(true) {
+        t = blockIdx.x;
+        if (p.split > 1) {  // a cluster for each tile
+            t /= (uint32_t)p.split;
+            step /= (uint32_t)p.split;
+        }
         mt = (uint32_t)(p.M + width - 1) / (uint32_t)width;
         nt = (uint32_t)(p.N + 127) / 128;
         total = mt * nt * (uint32_t)p.batch;
+        place();
     }
     __device__ __forceinline__ void place() {
-        const uint32_t r = t / nt;
-        n0 = (int)(t - r * nt) * 128;
+        uint32_t r = 0;
+        n0 = (int)t;
+        if (t >= nt) {
+            r = t / nt;
+            n0 = (int)(t - r * nt);
+        }
+        n0 *= 128;
         e = mt == 1 ? (int)r : (int)(r / mt);
         m0 = (int)(r - (uint32_t)e * mt) * width;
     }
     __device__ __forceinline__ bool next() {
         for (; t < total; t += step) {
-            place();
+            if (!placed) place();
+            placed = false;
             valid = min(width, valid_rows(p, e) - m0);
             if (valid > 0) {
                 t += step;
@@ -165,6 +192,57 @@ struct NarrowWalk {
         return false;
     }
 };
+
+// A cluster's partial sums of one tile added up and stored: every CTA takes
+// vectors of four outputs in turn, and adds them in the order of the ranks.
+// B >= split: eight loads from the peers are under way at a time, of one or
+// several vectors.
+template <int B, int W, int NT, int THREADS, bool BF16>
+__device__ __forceinline__ void add_parts(const Fp4MmParams &p, const NarrowWalk &w, uint32_t base,
+                                          int rank) {
+    constexpr int V = 8 / B;
+    const float xt = MM_XT(p, w.e);
+    float alpha[W];
+#pragma unroll
+    for (int u = 0; u < W; ++u) alpha[u] = __fmul_rn(xt, MM_WT(p, u, w.e));
+    const int vecs = w.valid * 32, step = p.split * THREADS;
+    for (int q0 = rank * THREADS + (int)threadIdx.x; q0 < vecs; q0 += V * step) {
+        float v[V][W][4];
+#pragma unroll
+        for (int u = 0; u < W; ++u) {
+            float4 f[V][B];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int q = q0 + i * step;
+                const uint32_t a = base + ((u * NT + (q >> 5)) * 128 + (q & 31) * 4) * 4;
+#pragma unroll
+                for (int r = 0; r < B; ++r)
+                    if (r < p.split && q < vecs) f[i][r] = dev::peer_ld4(dev::peer_addr(a, r));
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float4 s = f[i][0];
+#pragma unroll
+                for (int r = 1; r < B; ++r)
+                    if (r < p.split) {
+                        s.x += f[i][r].x, s.y += f[i][r].y;
+                        s.z += f[i][r].z, s.w += f[i][r].w;
+                    }
+                v[i][u][0] = s.x * alpha[u], v[i][u][1] = s.y * alpha[u];
+                v[i][u][2] = s.z * alpha[u], v[i][u][3] = s.w * alpha[u];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int q = q0 + i * step, o = w.n0 + (q & 31) * 4;
+            if (q >= vecs || o >= p.N) continue;
+            if constexpr (W == 2)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[i][0][j] = silu(v[i][0][j]) * v[i][W - 1][j];
+            store4<BF16>(p, w.e, w.m0 + (q >> 5), o, v[i][0]);
+        }
+    }
+}
 
 template <int FMT, bool GATED, bool BF16, int NT>
 __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
@@ -179,9 +257,12 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
     uint8_t *ring = raw + ((1024u - (dev::smem_addr(raw) & 1023u)) & 1023u);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = (int)(blockIdx.x % (unsigned)p.split);
-    const int k0 = (int)((int64_t)p.stages_k * rank / p.split);
-    const int k1 = (int)((int64_t)p.stages_k * (rank + 1) / p.split);
+    const uint32_t split = (uint32_t)p.split, rank = split > 1 ? dev::cluster_rank() : 0;
+    int k0 = 0, k1 = p.stages_k;  // this CTA's stages (fewer than 2^23)
+    if (split > 1) {
+        k0 = (int)((uint32_t)p.stages_k * rank / split);
+        k1 = (int)((uint32_t)p.stages_k * (rank + 1) / split);
+    }
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             dev::mbar_init(&full[s], 1);
@@ -195,13 +276,12 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
         dev::mbar_init(&done, 1);
         abort_flag = 0;
         dev::fence_mbar_init();
-        dev::prefetch_tensormap(&p.x);
+        dev::prefetch_tensormap(&p.x);  // that of the scales as well costs 0.3 us
     }
     if (warp == 1) dev::tmem_alloc<1>(&tmem_at, S::kCols);
     NarrowWalk w(p, NT);
     auto at = [&](int map) { return (p.moves >> map) & 1u ? w.e : 0; };
     if (warp == 2 && lane == 0) {  // the weight's first stages on their way to L2
-        w.place();
         for (int k = k0; k < k1 && k < k0 + S::kStages; ++k)
 #pragma unroll
             for (int v = 0; v < S::W; ++v) {
@@ -222,15 +302,31 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
         }
     };
     float *part = reinterpret_cast<float *>(ring);  // [weight][token][128 outputs]
+    // Every other 16 columns of this warp's lanes of the sums to `part`.  (The
+    // ring is free: every stage was multiplied.)
+    auto to_part = [&](int valid, int first) {
+        const uint32_t d = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+#pragma unroll
+        for (int c = 0; c < S::kSums; c += 16) {
+            if (c % NT >= valid || (c / 16 & 1) != first) continue;
+            uint32_t v[16];
+            dev::tmem_ld16(d + c, v);
+            dev::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                part[(c + j) * 128 + (warp & 3) * 32 + lane] = __uint_as_float(v[j]);
+        }
+    };
 
     if (warp == 0 && lane == 0) {
         bool dropped = false, ok = true;
         int i = 0;  // stages loaded
+        Slot<S::kStages> s;
         while (ok && w.next()) {
-            for (int k = k0; k < k1; ++k, ++i) {
-                const int st = i % S::kStages, round = i / S::kStages;
-                if (round > 0 && !dev::mbar_wait_bounded(&empty[st], (round - 1) & 1,
-                                                         p.wait_limit_ns, &abort_flag)) {
+            for (int k = k0; k < k1; ++k, ++i, s.next()) {
+                const int st = s.at;
+                if (i >= S::kStages && !dev::mbar_wait_bounded(&empty[st], s.parity ^ 1,
+                                                               p.wait_limit_ns, &abort_flag)) {
                     gave_up();
                     ok = false;
                     break;
@@ -265,58 +361,60 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
     } else if (warp == 1 && lane == 0) {
         constexpr uint32_t word = dev::mma_word(FMT, 128, NT);
         bool ok = true;
-        int i = 0, n = 0;  // stages, tiles
-        for (; ok && w.next(); ++n) {
-            const int acc = n % S::kAcc;
-            if (n >= S::kAcc && !dev::mbar_wait_bounded(&freed[acc], (n / S::kAcc - 1) & 1,
+        int n = 0;  // tiles
+        Slot<S::kStages> s;
+        Slot<S::kSfBufs> f;
+        Slot<S::kAcc> acc;
+        const uint64_t first = dev::operand_desc(dev::smem_addr(ring));
+        for (; ok && w.next(); ++n, acc.next()) {
+            if (n >= S::kAcc && !dev::mbar_wait_bounded(&freed[acc.at], acc.parity ^ 1,
                                                         p.wait_limit_ns, &abort_flag)) {
                 gave_up();
                 break;
             }
-            for (int k = k0; k < k1; ++k, ++i) {
-                const int st = i % S::kStages;
-                if (!dev::mbar_wait_bounded(&full[st], (i / S::kStages) & 1, p.wait_limit_ns,
-                                            &abort_flag) ||
-                    !dev::mbar_wait_bounded(&scaled[i % S::kSfBufs], (i / S::kSfBufs) & 1,
-                                            p.wait_limit_ns, &abort_flag)) {
+            const uint32_t d = tmem + acc.at * S::kSums;
+            for (int k = k0; k < k1; ++k, s.next(), f.next()) {
+                const uint64_t wd = first + (uint32_t)(s.at * (S::kStage >> 4));
+                const uint64_t xd = wd + (S::W * S::kCodesW >> 4);
+                const uint32_t sw = tmem + S::kAcc * S::kSums + f.at * S::kSfCols;
+                const uint32_t sx = sw + 4 * S::KT * S::W;
+                const int steps = p.mma_k - 4 * k;  // 64-column steps left
+                if (!dev::mbar_wait_bounded(&full[s.at], s.parity, p.wait_limit_ns, &abort_flag) ||
+                    !dev::mbar_wait_bounded(&scaled[f.at], f.parity, p.wait_limit_ns,
+                                            &abort_flag)) {
                     gave_up();
                     ok = false;
                     break;
                 }
                 dev::tc_fence_after();
-                const uint32_t b = dev::smem_addr(ring + st * S::kStage);
-                const uint32_t sw =
-                    tmem + S::kAcc * S::kSums + (i % S::kSfBufs) * S::kSfCols;
-                const uint32_t sx = sw + 4 * S::KT * S::W;
-                const uint64_t xd = dev::operand_desc(b + S::W * S::kCodesW);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (4 * k + j >= p.mma_k) break;
+                    if (j >= steps) break;
                     const int t = j * S::KT / 4;
-                    const uint32_t wd = dev::mma_word_id(word, FMT == FP8BQ_MXFP4 ? 2 * (j & 1) : 0);
 #pragma unroll
                     for (int v = 0; v < S::W; ++v)
-                        dev::mma_fp4<FMT, 1>(tmem + acc * S::kSums + v * NT,
-                                             dev::operand_desc(b + v * S::kCodesW) + 2 * j,
-                                             xd + 2 * j, wd, sw + 4 * (v * S::KT + t),
-                                             sx + 4 * t * S::XT, k > k0 || j > 0);
+                        dev::mma_fp4<FMT, 1>(
+                            d + v * NT, wd + (v * S::kCodesW >> 4) + 2 * j, xd + 2 * j,
+                            dev::mma_word_id(word, FMT == FP8BQ_MXFP4 ? 2 * (j & 1) : 0),
+                            sw + 4 * (v * S::KT + t), sx + 4 * t * S::XT, j > 0 || k > k0);
                 }
-                dev::mma_commit<1>(&empty[st]);
+                dev::mma_commit<1>(&empty[s.at]);
             }
-            dev::mma_commit<1>(&sums[acc]);
+            dev::mma_commit<1>(&sums[acc.at]);
         }
         dev::mma_commit<1>(&done);
         if (!dev::mbar_wait_bounded(&done, 0, kDrainNs, nullptr)) atomicOr(&g_fp4_error_word, 2u);
     } else if (warp >= 4 && warp < 8) {
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
         bool ok = true;
+        Slot<S::kStages> s, old;  // `old`: kSfBufs stages behind
+        Slot<S::kSfBufs> f;
         for (int i = 0; ok && w.next();) {
-            for (int k = k0; k < k1; ++k, ++i) {
-                const int st = i % S::kStages, b = i % S::kSfBufs;
-                bool here = dev::mbar_wait_bounded(&full[st], (i / S::kStages) & 1, p.wait_limit_ns,
+            for (int k = k0; k < k1; ++k, ++i, s.next(), f.next()) {
+                bool here = dev::mbar_wait_bounded(&full[s.at], s.parity, p.wait_limit_ns,
                                                    &abort_flag);
                 const uint8_t *sf =
-                    ring + st * S::kStage + S::W * S::kCodesW + S::kCodesX + lane * 16;
+                    ring + s.at * S::kStage + S::W * S::kCodesW + S::kCodesX + lane * 16;
                 uint4 v[S::kTiles];  // of each weight, then tile by tile of the tokens
 #pragma unroll
                 for (int t = 0; t < S::KT; ++t) {
@@ -329,10 +427,9 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
                             *(const uint4 *)(sf + (S::W + x) * S::SF + t * kFp4TileBytes);
                 }
                 if (i >= S::kSfBufs) {  // the products that read this buffer are done
-                    const int o = i - S::kSfBufs;
-                    here = here && dev::mbar_wait_bounded(&empty[o % S::kStages],
-                                                          (o / S::kStages) & 1, p.wait_limit_ns,
-                                                          &abort_flag);
+                    here = here && dev::mbar_wait_bounded(&empty[old.at], old.parity,
+                                                          p.wait_limit_ns, &abort_flag);
+                    old.next();
                 }
                 if (!__all_sync(0xffffffffu, here)) {
                     if (lane == 0) gave_up();
@@ -341,34 +438,35 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
                 }
                 dev::tc_fence_after();
                 scales_to_tmem<S::kTiles>(
-                    tmem + quarter + S::kAcc * S::kSums + b * S::kSfCols, v);
+                    tmem + quarter + S::kAcc * S::kSums + f.at * S::kSfCols, v);
                 dev::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) dev::mbar_arrive(&scaled[b]);
+                if (lane == 0) dev::mbar_arrive(&scaled[f.at]);
+            }
+        }
+        if (split > 1 && ok && S::kSums > 16 && w.valid > 0) {  // the tile's other half
+            const bool here =
+                dev::mbar_wait_bounded(&sums[0], 0, 2 * p.wait_limit_ns, &abort_flag);
+            if (__all_sync(0xffffffffu, here)) {
+                dev::tc_fence_after();
+                to_part(w.valid, 1);
+            } else if (lane == 0) {
+                gave_up();
             }
         }
     } else if (warp >= 8) {
         const int row = (warp & 3) * 32 + lane;  // of the weight's 128
-        for (int n = 0; w.next(); ++n) {
-            const int acc = n % S::kAcc;
-            const bool here = dev::mbar_wait_bounded(&sums[acc], (n / S::kAcc) & 1,
+        for (Slot<S::kAcc> acc; w.next(); acc.next()) {
+            const bool here = dev::mbar_wait_bounded(&sums[acc.at], acc.parity,
                                                      2 * p.wait_limit_ns, &abort_flag);
             if (!__all_sync(0xffffffffu, here)) {
                 if (lane == 0) gave_up();
                 break;
             }
             dev::tc_fence_after();
-            const uint32_t d = tmem + acc * S::kSums + ((uint32_t)((warp & 3) * 32) << 16);
-            if (p.split > 1) {  // the ring is free: every stage was multiplied
-#pragma unroll
-                for (int c = 0; c < S::kSums; c += 16) {
-                    if (c % NT >= w.valid) continue;
-                    uint32_t v[16];
-                    dev::tmem_ld16(d + c, v);
-                    dev::tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) part[(c + j) * 128 + row] = __uint_as_float(v[j]);
-                }
+            const uint32_t d = tmem + acc.at * S::kSums + ((uint32_t)((warp & 3) * 32) << 16);
+            if (split > 1) {
+                to_part(w.valid, 0);
                 continue;
             }
             const float xt = MM_XT(p, w.e), alpha = __fmul_rn(xt, MM_WT(p, 0, w.e));
@@ -384,7 +482,7 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
                 if (c + 16 >= w.valid) {
                     dev::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) dev::mbar_arrive(&freed[acc]);
+                    if (lane == 0) dev::mbar_arrive(&freed[acc.at]);
                 }
                 float v[16];
 #pragma unroll
@@ -426,36 +524,20 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
     }
     __syncwarp();
     dev::tc_fence_before();
-    NarrowWalk one(p, NT);
-    if (p.split > 1 && one.next()) {  // the same for every CTA of a cluster
-        dev::cluster_sync();
-        const float xt = MM_XT(p, one.e);
-        float alpha[S::W];
-#pragma unroll
-        for (int v = 0; v < S::W; ++v) alpha[v] = __fmul_rn(xt, MM_WT(p, v, one.e));
-        const uint32_t base = dev::smem_addr(part);
-        for (int q = rank * S::kThreads + tid; !abort_flag && q < one.valid * 32;
-             q += p.split * S::kThreads) {
-            const int t = q >> 5, o = one.n0 + (q & 31) * 4;
-            if (o >= p.N) continue;
-            float v[S::W][4];
-#pragma unroll
-            for (int u = 0; u < S::W; ++u) {
-                const uint32_t a = base + ((u * NT + t) * 128 + (q & 31) * 4) * 4;
-                float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int r = 0; r < p.split; ++r) {
-                    const float4 f = dev::peer_ld4(dev::peer_addr(a, r));
-                    s.x += f.x, s.y += f.y, s.z += f.z, s.w += f.w;
-                }
-                v[u][0] = s.x * alpha[u], v[u][1] = s.y * alpha[u];
-                v[u][2] = s.z * alpha[u], v[u][3] = s.w * alpha[u];
+    if (split > 1) {
+        NarrowWalk one(p, NT);
+        if (one.next()) {  // the same for every CTA of a cluster
+            dev::cluster_sync();
+            const uint32_t base = dev::smem_addr(part);
+            // few tokens: one way only, a short kernel starts sooner
+            if (!abort_flag) {
+                if (NT >= 64 && split <= 2)
+                    add_parts<2, S::W, NT, S::kThreads, BF16>(p, one, base, rank);
+                else
+                    add_parts<8, S::W, NT, S::kThreads, BF16>(p, one, base, rank);
             }
-            if constexpr (GATED)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[0][j] = silu(v[0][j]) * v[S::W - 1][j];
-            store4<BF16>(p, one.e, one.m0 + t, o, v[0]);
+            dev::cluster_sync();  // peers may still read this CTA's sums
         }
-        dev::cluster_sync();  // peers may still read this CTA's sums
     }
     __syncthreads();
     if (warp == 1) dev::tmem_dealloc<1>(tmem, S::kCols);
@@ -590,8 +672,13 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
         dev::mbar_init(&done, 1);
         abort_flag = 0;
         dev::fence_mbar_init();
-        dev::prefetch_tensormap(&p.w[0]);
+    }
+    if (warp == 2 && lane == 0) {
         dev::prefetch_tensormap(&p.x);
+        dev::prefetch_tensormap(&p.xs);
+        dev::prefetch_tensormap(&p.w[GATED ? rank : 0]);
+        dev::prefetch_tensormap(&p.ws[0]);
+        if (GATED) dev::prefetch_tensormap(&p.ws[1]);
     }
     if (warp == 1) dev::tmem_alloc<2>(&tmem_at, 512);
     dev::tc_fence_before();
@@ -612,11 +699,12 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
         auto at = [&](int map) { return (p.moves >> map) & 1u ? w.e : 0; };
         bool dropped = false, ok = true;
         int i = 0;  // stages loaded
+        Slot<S::kStages> s;
         while (ok && w.next()) {
-            for (int k = 0; k < p.stages_k; ++k, ++i) {
-                const int st = i % S::kStages, round = i / S::kStages;
-                if (round > 0 && !dev::mbar_wait_bounded(&empty[st], (round - 1) & 1,
-                                                         p.wait_limit_ns, &abort_flag)) {
+            for (int k = 0; k < p.stages_k; ++k, ++i, s.next()) {
+                const int st = s.at;
+                if (i >= S::kStages && !dev::mbar_wait_bounded(&empty[st], s.parity ^ 1,
+                                                               p.wait_limit_ns, &abort_flag)) {
                     gave_up();
                     ok = false;
                     break;
@@ -656,40 +744,41 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
     } else if (warp == 1 && lane == 0 && rank == 0) {
         constexpr uint32_t word = dev::mma_word(FMT, 256, 256);
         bool ok = true;
-        int i = 0, n = 0;  // stages, tiles
+        int n = 0;  // tiles
+        Slot<S::kStages> s;
+        Slot<S::kSfBufs> f;
+        const uint64_t first = dev::operand_desc(dev::smem_addr(ring));
         for (; ok && w.next(); ++n) {
             if (n > 0 && !dev::mbar_wait_bounded(&drained, (n - 1) & 1, p.wait_limit_ns,
                                                  &abort_flag)) {
                 gave_up();
                 break;
             }
-            dev::tc_fence_after();
             const uint32_t d = tmem + (n & 1) * S::kOther;
-            for (int k = 0; k < p.stages_k; ++k, ++i) {
-                const int st = i % S::kStages;
-                if (!dev::mbar_wait_bounded(&full[st], (i / S::kStages) & 1, p.wait_limit_ns,
-                                            &abort_flag) ||
-                    !dev::mbar_wait_bounded(&scaled[i % S::kSfBufs], (i / S::kSfBufs) & 1,
-                                            p.wait_limit_ns, &abort_flag)) {
+            for (int k = 0; k < p.stages_k; ++k, s.next(), f.next()) {
+                const uint64_t xd = first + (uint32_t)(s.at * (S::kStage >> 4));
+                const uint64_t wd = xd + (S::kCodes >> 4);
+                const uint32_t sx = tmem + S::kScales + f.at * S::kSfCols;
+                const uint32_t sw = sx + 4 * S::KT;
+                const int steps = p.mma_k - 4 * k;  // 64-column steps left
+                if (!dev::mbar_wait_bounded(&full[s.at], s.parity, p.wait_limit_ns, &abort_flag) ||
+                    !dev::mbar_wait_bounded(&scaled[f.at], f.parity, p.wait_limit_ns,
+                                            &abort_flag)) {
                     gave_up();
                     ok = false;
                     break;
                 }
                 dev::tc_fence_after();
-                const uint32_t at = dev::smem_addr(ring + st * S::kStage);
-                const uint32_t sx = tmem + S::kScales + (i % S::kSfBufs) * S::kSfCols;
-                const uint32_t sw = sx + 4 * S::KT;
-                const uint64_t xd = dev::operand_desc(at), wd = dev::operand_desc(at + S::kCodes);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (4 * k + j >= p.mma_k) break;
+                    if (j >= steps) break;
                     const int t = j * S::KT / 4;
                     dev::mma_fp4<FMT, 2>(
                         d, xd + 2 * j, wd + 2 * j,
                         dev::mma_word_id(word, FMT == FP8BQ_MXFP4 ? 2 * (j & 1) : 0), sx + 4 * t,
-                        sw + 8 * t, k + j > 0);
+                        sw + 8 * t, j > 0 || k > 0);
                 }
-                dev::mma_commit<2>(&empty[st]);
+                dev::mma_commit<2>(&empty[s.at]);
             }
             dev::mma_commit<2>(&sums);
         }
@@ -698,12 +787,13 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
     } else if (warp >= 4 && warp < 8) {
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
         bool ok = true;
+        Slot<S::kStages> s, old;  // `old`: kSfBufs stages behind
+        Slot<S::kSfBufs> f;
         for (int i = 0; ok && w.next();) {
-            for (int k = 0; k < p.stages_k; ++k, ++i) {
-                const int st = i % S::kStages, b = i % S::kSfBufs;
-                bool here = dev::mbar_wait_bounded(&landed[st], (i / S::kStages) & 1,
-                                                   p.wait_limit_ns, &abort_flag);
-                const uint8_t *sf = ring + st * S::kStage + 2 * S::kCodes + lane * 16;
+            for (int k = 0; k < p.stages_k; ++k, ++i, s.next(), f.next()) {
+                bool here = dev::mbar_wait_bounded(&landed[s.at], s.parity, p.wait_limit_ns,
+                                                   &abort_flag);
+                const uint8_t *sf = ring + s.at * S::kStage + 2 * S::kCodes + lane * 16;
                 uint4 v[3 * S::KT];  // of the tokens, then tile by tile of the weight's two rows
 #pragma unroll
                 for (int t = 0; t < S::KT; ++t) {
@@ -712,10 +802,9 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
                     v[S::KT + 2 * t + 1] = *(const uint4 *)(sf + 2 * S::SF + t * kFp4TileBytes);
                 }
                 if (i >= S::kSfBufs) {  // the products that read this buffer are done
-                    const int o = i - S::kSfBufs;
-                    here = here && dev::mbar_wait_bounded(&empty[o % S::kStages],
-                                                          (o / S::kStages) & 1, p.wait_limit_ns,
-                                                          &abort_flag);
+                    here = here && dev::mbar_wait_bounded(&empty[old.at], old.parity,
+                                                          p.wait_limit_ns, &abort_flag);
+                    old.next();
                 }
                 if (!__all_sync(0xffffffffu, here)) {
                     if (lane == 0) gave_up();
@@ -723,10 +812,10 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
                     break;
                 }
                 dev::tc_fence_after();
-                scales_to_tmem<3 * S::KT>(tmem + quarter + S::kScales + b * S::kSfCols, v);
+                scales_to_tmem<3 * S::KT>(tmem + quarter + S::kScales + f.at * S::kSfCols, v);
                 dev::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) dev::peer_arrive(dev::peer_addr(dev::smem_addr(&scaled[b]), 0));
+                if (lane == 0) dev::peer_arrive(dev::peer_addr(dev::smem_addr(&scaled[f.at]), 0));
             }
         }
     } else if (warp >= 8) {
