@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
         int n = 0;  // tiles
         Slot<S::kStages> s;
         Slot<S::kSfBufs> f;
+        bool ready = false;
         Slot<S::kAcc> acc;
         const uint64_t first = dev::operand_desc(dev::smem_addr(ring));
         for (; ok && w.next(); ++n, acc.next()) {
@@ -373,15 +374,14 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
                 break;
             }
             const uint32_t d = tmem + acc.at * S::kSums;
-            for (int k = k0; k < k1; ++k, s.next(), f.next()) {
+            for (int k = k0; k < k1; ++k, s.next()) {
                 const uint64_t wd = first + (uint32_t)(s.at * (S::kStage >> 4));
                 const uint64_t xd = wd + (S::W * S::kCodesW >> 4);
                 const uint32_t sw = tmem + S::kAcc * S::kSums + f.at * S::kSfCols;
                 const uint32_t sx = sw + 4 * S::KT * S::W;
                 const int steps = p.mma_k - 4 * k;  // 64-column steps left
-                if (!dev::mbar_wait_bounded(&full[s.at], s.parity, p.wait_limit_ns, &abort_flag) ||
-                    !dev::mbar_wait_bounded(&scaled[f.at], f.parity, p.wait_limit_ns,
-                                            &abort_flag)) {
+                if (!ready && !dev::mbar_wait_bounded(&scaled[f.at], f.parity, p.wait_limit_ns,
+                                                      &abort_flag)) {
                     gave_up();
                     ok = false;
                     break;
@@ -398,6 +398,8 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
                             dev::mma_word_id(word, FMT == FP8BQ_MXFP4 ? 2 * (j & 1) : 0),
                             sw + 4 * (v * S::KT + t), sx + 4 * t * S::XT, j > 0 || k > k0);
                 }
+                f.next();
+                ready = dev::mbar_try_wait(&scaled[f.at], f.parity);  // the next stage's
                 dev::mma_commit<1>(&empty[s.at]);
             }
             dev::mma_commit<1>(&sums[acc.at]);
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
 // warps 4-7 bring the scales into tensor memory, warps 8-15 store; warp 1 of
 // the first CTA issues the products of both.  The sums of successive tiles
 // alternate between columns [0, 256) and [160, 416), so the next tile is
-// multiplied while this one is stored; the 96 columns that both use are stored
+// multiplied while this one is stored; the 96 columns that both use are read
 // first, and the next tile waits for those alone.  The scales' buffers take
 // the last 96 columns.
 //
@@ -579,19 +581,19 @@ struct Wide {
     static_assert(kSfBufs >= 2 && kSfBufs <= kStages, "scale buffers");
 };
 
-// 32 consecutive outputs of a row, from column n; `align` bytes.
+// 16 consecutive outputs of a row, from column n.
 template <bool BF16>
-__device__ __forceinline__ void store32(const Fp4MmParams &p, int64_t e, int64_t m, int n,
-                                        const float (&v)[32]) {
+__device__ __forceinline__ void store16(const Fp4MmParams &p, int64_t e, int64_t m, int n,
+                                        const float (&v)[16]) {
     constexpr int ES = BF16 ? 2 : 4, PER = 32 / ES;            // outputs in 32 bytes
     char *dst = (char *)p.out + (e * p.obs + m * p.ldo + n) * ES;
 #pragma unroll
-    for (int c = 0; c < 32; c += PER, dst += 32) {
+    for (int c = 0; c < 16; c += PER, dst += 32) {
         uint32_t w[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            w[j] = BF16 ? bf16x2(v[(c + 2 * j) & 31], v[(c + 2 * j + 1) & 31])
-                        : __float_as_uint(v[(c + j) & 31]);
+            w[j] = BF16 ? bf16x2(v[(c + 2 * j) & 15], v[(c + 2 * j + 1) & 15])
+                        : __float_as_uint(v[(c + j) & 15]);
         if (n + c + PER <= p.N && p.store_align >= 16) {
             if (!FP8BQ_IN(MM_SPAN(p.out, p.out_bytes), dst, 32)) continue;
             if (p.store_align >= 32) {
@@ -747,6 +749,7 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
         int n = 0;  // tiles
         Slot<S::kStages> s;
         Slot<S::kSfBufs> f;
+        bool ready = false;
         const uint64_t first = dev::operand_desc(dev::smem_addr(ring));
         for (; ok && w.next(); ++n) {
             if (n > 0 && !dev::mbar_wait_bounded(&drained, (n - 1) & 1, p.wait_limit_ns,
@@ -755,15 +758,14 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
                 break;
             }
             const uint32_t d = tmem + (n & 1) * S::kOther;
-            for (int k = 0; k < p.stages_k; ++k, s.next(), f.next()) {
+            for (int k = 0; k < p.stages_k; ++k, s.next()) {
                 const uint64_t xd = first + (uint32_t)(s.at * (S::kStage >> 4));
                 const uint64_t wd = xd + (S::kCodes >> 4);
                 const uint32_t sx = tmem + S::kScales + f.at * S::kSfCols;
                 const uint32_t sw = sx + 4 * S::KT;
                 const int steps = p.mma_k - 4 * k;  // 64-column steps left
-                if (!dev::mbar_wait_bounded(&full[s.at], s.parity, p.wait_limit_ns, &abort_flag) ||
-                    !dev::mbar_wait_bounded(&scaled[f.at], f.parity, p.wait_limit_ns,
-                                            &abort_flag)) {
+                if (!ready && !dev::mbar_wait_bounded(&scaled[f.at], f.parity, p.wait_limit_ns,
+                                                      &abort_flag)) {
                     gave_up();
                     ok = false;
                     break;
@@ -778,6 +780,8 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
                         dev::mma_word_id(word, FMT == FP8BQ_MXFP4 ? 2 * (j & 1) : 0), sx + 4 * t,
                         sw + 8 * t, j > 0 || k > 0);
                 }
+                f.next();
+                ready = dev::mbar_try_wait(&scaled[f.at], f.parity);  // the next stage's
                 dev::mma_commit<2>(&empty[s.at]);
             }
             dev::mma_commit<2>(&sums);
@@ -793,6 +797,9 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
             for (int k = 0; k < p.stages_k; ++k, ++i, s.next(), f.next()) {
                 bool here = dev::mbar_wait_bounded(&landed[s.at], s.parity, p.wait_limit_ns,
                                                    &abort_flag);
+                if (rank == 0)
+                    here = here && dev::mbar_wait_bounded(&full[s.at], s.parity, p.wait_limit_ns,
+                                                          &abort_flag);
                 const uint8_t *sf = ring + s.at * S::kStage + 2 * S::kCodes + lane * 16;
                 uint4 v[3 * S::KT];  // of the tokens, then tile by tile of the weight's two rows
 #pragma unroll
@@ -834,39 +841,53 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
             const bool in = m < w.valid;
             const float xt = MM_XT(p, w.e), alpha = __fmul_rn(xt, MM_WT(p, 0, w.e));
             const float alpha1 = GATED ? __fmul_rn(xt, MM_WT(p, 1, w.e)) : 0.0f;
-            // runs of 32 columns, the shared ones (5-7 of even tiles, 0-2 of
-            // odd ones) first; the two warps of a quarter take turns
+            // Runs of 16 columns, every other one of them this warp's, from
+            // the side whose columns the next tile shares: those (gated: the
+            // up sums of even tiles, the gate's of odd ones) are all read
+            // before anything is stored.
             constexpr int kRuns = GATED ? 4 : 8;
-#pragma unroll 1
-            for (int j = half; j < kRuns; j += 2) {
-                const int c = (n & 1) ? j : kRuns - 1 - j;
-                float v[32];
-                if constexpr (GATED) {
-                    uint32_t g[32], u[32];
-                    dev::tmem_ld32(d + 32 * c, g);
-                    dev::tmem_ld32(d + 128 + 32 * c, u);
-                    dev::tmem_ld_wait();
-                    if (j == 2 - half) {  // its last run of the first three
-                        dev::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) dev::peer_arrive(drained_bar);
-                    }
+            const bool odd = n & 1;
+            auto run = [&](int i) { return half + 2 * (odd ? i : kRuns - 1 - i); };
+            const uint32_t shared = d + (GATED && !odd ? 128 : 0);
+            const uint32_t others = d + (GATED && odd ? 128 : 0);
+            uint32_t pre[3][16];
 #pragma unroll
-                    for (int q = 0; q < 32; ++q)
-                        v[q] = silu(__uint_as_float(g[q]) * alpha) * (__uint_as_float(u[q]) * alpha1);
-                } else {
-                    uint32_t g[32];
-                    dev::tmem_ld32(d + 32 * c, g);
-                    dev::tmem_ld_wait();
-                    if (j == 2 - half) {  // its last run of the first three
-                        dev::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) dev::peer_arrive(drained_bar);
-                    }
+            for (int i = 0; i < 3; ++i) dev::tmem_ld16(shared + 16 * run(i), pre[i]);
+            dev::tmem_ld_wait();
+            dev::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) dev::peer_arrive(drained_bar);
+            auto store = [&](int i, const uint32_t (&x)[16], const uint32_t (&y)[16]) {
+                float v[16];
 #pragma unroll
-                    for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(g[q]) * alpha;
+                for (int q = 0; q < 16; ++q) {
+                    if constexpr (GATED) {
+                        const float g = __uint_as_float(odd ? x[q] : y[q]);
+                        const float u = __uint_as_float(odd ? y[q] : x[q]);
+                        v[q] = silu(g * alpha) * (u * alpha1);
+                    } else {
+                        v[q] = __uint_as_float(x[q]) * alpha;
+                    }
                 }
-                if (in && w.n0 + 32 * c < p.N) store32<BF16>(p, w.e, m, w.n0 + 32 * c, v);
+                const int c = w.n0 + 16 * run(i);
+                if (in && c < p.N) store16<BF16>(p, w.e, m, c, v);
+            };
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                uint32_t y[16];
+                if constexpr (GATED) {
+                    dev::tmem_ld16(others + 16 * run(i), y);
+                    dev::tmem_ld_wait();
+                }
+                store(i, pre[i], GATED ? y : pre[i]);
+            }
+#pragma unroll 1
+            for (int i = 3; i < kRuns; ++i) {
+                uint32_t x[16], y[16];
+                dev::tmem_ld16(shared + 16 * run(i), x);
+                if constexpr (GATED) dev::tmem_ld16(others + 16 * run(i), y);
+                dev::tmem_ld_wait();
+                store(i, x, GATED ? y : x);
             }
         }
     }
