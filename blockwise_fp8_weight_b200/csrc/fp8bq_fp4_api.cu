@@ -325,8 +325,9 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     if (((__int128)(D.M + 15) / 16) * ((D.N + 127) / 128) * D.batch >= (1ll << 31))
         return FP8BQ_ERR_SHAPE;
 
-    const bool wide = D.M > 256;
-    const int tokens = fp4_narrow_tokens(D.M, gated);
+    const int64_t kb = fp4_row_bytes(D.K), stages = (kb + 127) / 128;
+    const int tokens = fp4_choose(D.M, D.N, stages, D.batch, gated);
+    const bool wide = tokens == 0;
     Fp4MmParams p;
     std::memset(&p, 0, sizeof p);
     bool ok = map_codes(mats[0], D, wide ? 128 : tokens, &p.x) && map_scales(mats[0], D, &p.xs);
@@ -347,8 +348,7 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     p.M = (int32_t)D.M;
     p.N = (int32_t)D.N;
     p.batch = (int32_t)D.batch;
-    const int64_t kb = fp4_row_bytes(D.K);
-    p.stages_k = (int32_t)((kb + 127) / 128);
+    p.stages_k = (int32_t)stages;
     p.mma_k = (int32_t)((kb + 31) / 32);
     p.split = 1;
     p.store_align = es;

@@ -102,7 +102,8 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t dst, const uint4 (&v)[TI
 // ============================================================== few tokens
 //
 // A CTA computes 128 outputs (rows of the weight, the M side of the tensor
-// core's tile) for NT tokens (its N side): few tokens cost few MMA columns,
+// core's tile) for NT tokens (its N side; tiles of 16 and 32 only where they
+// hold all tokens: scale tiles begin every 128): few tokens cost few MMA columns,
 // and the kernel is bound by the weight's bytes.
 //
 // Where the tiles are too few to keep every SM loading, a cluster of `split`
@@ -378,7 +379,8 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
                 const uint64_t wd = first + (uint32_t)(s.at * (S::kStage >> 4));
                 const uint64_t xd = wd + (S::W * S::kCodesW >> 4);
                 const uint32_t sw = tmem + S::kAcc * S::kSums + f.at * S::kSfCols;
-                const uint32_t sx = sw + 4 * S::KT * S::W;
+                // tokens 64-127 of a scale tile begin at its third column
+                const uint32_t sx = sw + 4 * S::KT * S::W + (NT == 64 ? (w.m0 & 64) >> 5 : 0);
                 const int steps = p.mma_k - 4 * k;  // 64-column steps left
                 if (!ready && !dev::mbar_wait_bounded(&scaled[f.at], f.parity, p.wait_limit_ns,
                                                       &abort_flag)) {
@@ -1032,10 +1034,51 @@ cudaError_t launch_fp4_mm_wide(const Fp4MmParams &p, int format, bool gated, boo
                                  : wide_format<FP8BQ_NVFP4>(p, gated, out_bf16, st);
 }
 
-int fp4_narrow_tokens(int64_t M, bool gated) {
-    for (int t : {16, 32, 64, 128})
-        if (M <= t) return t;
-    return gated ? 128 : 256;
+// The kernel for a product: the tile's width in tokens of the few-token kernel,
+// or 0 for the many-token one.  Up to 32 tokens the narrowest tile that holds
+// them; beyond, the one with the shortest estimate.  A call takes about
+//     begin + stage * (stages of a CTA) + again * (stages) * (rounds - 1)
+// microseconds, rounds = tiles over the tiles that run at once.  Fitted to
+// B200, 1000 x 4100 to 12288 x 4096 and 4096 x 12288, 64 to 2048 tokens, mxfp4
+// (measured, us, many-token / 64 / 128 / 256 wide tiles):
+//     515 tokens, 1000 x 4100    13.7 / 10.7 /  9.8 / 11.5
+//     256 tokens, 4096 x 4096    12.2 / 10.7 / 10.2 / 10.9
+//     256 tokens, 12288 x 4096   13.0 / 20.2 / 20.3 / 17.1
+//     300 tokens, 4096 x 12288   26.3 / 26.5 / 25.7 / 18.5
+//     1024 tokens, 6144 x 4096   20.5 / 29.1 / 27.6 / 30.3
+//     gated, 256 x 4096 x 4096   12.8 / 15.0 / 13.4
+//     gated, 64 x 12288 x 4096   21.3 / 15.8 / 15.9
+int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated) {
+    if (M <= 16) return 16;
+    if (M <= 32) return 32;
+    struct Cost {
+        int tokens;
+        double begin, stage, again;
+    };
+    static constexpr Cost plain[] = {
+        {0, 4.8, 0.45, 0.50}, {64, 6.2, 0.40, 0.45}, {128, 7.0, 0.36, 0.47}, {256, 8.6, 0.50, 0.90}};
+    static constexpr Cost both[] = {{0, 4.8, 0.47, 0.50}, {64, 8.3, 0.42, 0.57}, {128, 9.5, 0.55, 0.85}};
+    const double sms = sm_count();
+    int best = 0;
+    double least = 0;
+    for (int i = 0; i < (gated ? 3 : 4); ++i) {
+        const Cost &c = gated ? both[i] : plain[i];
+        const int64_t rows = c.tokens ? c.tokens : 256, cols = c.tokens || gated ? 128 : 256;
+        const double tiles = (double)((M + rows - 1) / rows) * (double)((N + cols - 1) / cols) * batch;
+        const double once = c.tokens == 0 ? sms / 2 : c.tokens == 64 && !gated ? 2 * sms : sms;
+        double share = (double)stages;  // stages of a CTA where a cluster splits K
+        if (c.tokens)
+            for (int s : {2, 3, 4, 6, 8})  // clusters of more than two leave some SMs out
+                if (s <= stages && tiles * s <= once * (s == 2 ? 1.0 : s == 8 ? 0.82 : 0.9))
+                    share = (double)((stages + s - 1) / s);
+        const double rounds = (double)(int64_t)((tiles + once - 1) / once);
+        const double t = c.begin + c.stage * share + c.again * stages * (rounds - 1);
+        if (i == 0 || t < least) {
+            least = t;
+            best = c.tokens;
+        }
+    }
+    return best;
 }
 
 cudaError_t launch_fp4_mm_narrow(const Fp4MmParams &p, int format, bool gated, bool out_bf16,

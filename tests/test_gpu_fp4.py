@@ -213,7 +213,8 @@ def rounded(y, dtype):
 SHAPES = [(1, 1, 1), (1, 128, 256), (16, 128, 64), (1, 300, 4096), (7, 129, 96), (17, 256, 1000),
           (33, 64, 2048), (64, 500, 320), (65, 128, 128), (100, 260, 544), (128, 128, 512),
           (129, 384, 256), (256, 200, 800), (257, 256, 1056), (300, 1000, 96), (515, 130, 4100),
-          (1000, 640, 288), (1, 8, 8192)]
+          (1000, 640, 288), (1, 8, 8192), (515, 1000, 4100), (200, 4096, 512), (90, 3000, 768),
+          (300, 256, 8192), (40, 136, 2080)]
 
 
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
@@ -265,7 +266,7 @@ def gated_close(y, g, u, out):
 
 GATED = [(1, 1, 1), (1, 128, 256), (16, 64, 512), (5, 300, 1100), (32, 129, 96), (50, 256, 320),
          (64, 128, 128), (77, 1000, 64), (128, 140, 288), (129, 256, 256), (300, 130, 1000),
-         (1, 24, 4096), (700, 384, 544)]
+         (1, 24, 4096), (700, 384, 544), (515, 1000, 2048), (100, 2500, 512), (40, 72, 2080)]
 
 
 def gated_operands(M, N, K, fmt, E=0):
