@@ -671,9 +671,12 @@ def _fp4_record(w, name: str, format: str, block: int, tensor_scale):
         raise ValueError(f"{name}: expected a 2-D weight or a 3-D stack of expert weights")
     if K > 1 and w.stride(-1) != 1:
         raise ValueError(f"{name}: the last dimension of the input must have unit stride")
+    ld = w.stride(-2) if M > 1 else K
+    if ld < K:
+        raise ValueError(f"{name}: the rows of the input overlap")
     t, ts = _fp4_tensor_scale(tensor_scale, E, format, f"{name}'s tensor scale")
     return ((*lead, M, 16 * (-(-K // 32))), (*lead, -(-M // 128), -(-K // (4 * block)), 32, 16),
-            (t, M, K, max(w.stride(-2), K) if M > 1 else K, E, xbs, ts, _dtype_code(w),
+            (t, M, K, ld, E, xbs, ts, _dtype_code(w),
              _FP4_FORMATS[format][0]))
 
 
@@ -845,7 +848,9 @@ def _fp4_product(what, a, b, up, format, out_dtype, rows, out, stream):
         st = out.stride()
         if N > 1 and st[-1] != 1:
             raise ValueError("the last dimension of out must have unit stride")
-        ld, obs = (max(st[-2], N) if M > 1 else N), (st[0] if dim == 3 else 0)
+        ld, obs = (st[-2] if M > 1 else N), (st[0] if dim == 3 else 0)
+        if ld < N:
+            raise ValueError("the rows of out overlap")
     st = getattr(L, "fp8bq_fp4_" + what)(_FP4_MATMUL_DESC.pack(
         *fa, *fb, *fu, out.data_ptr(), 0 if rows is None else rows.data_ptr(), M, N, 2 * kb,
         E if dim == 3 else 1, ld, obs, fmt,

@@ -290,9 +290,12 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     if (!dtype_ok(D.dtype_out)) return FP8BQ_ERR_DTYPE;
     if (!format_ok(D.format)) return FP8BQ_ERR_ARG;
     if (D.M < 0 || D.N < 0 || D.batch < 0 || D.K < 1 || D.ld_out < D.N || D.M > kMaxDim ||
-        D.N > kMaxDim || D.K > kMaxDim || D.batch > 65535 || fp4_tiles_m(D.M) > 65535)
+        D.N > kMaxDim || D.K > kMaxDim || D.batch > kMaxDim)
         return FP8BQ_ERR_SHAPE;
     if (D.M == 0 || D.N == 0 || D.batch == 0) return FP8BQ_OK;
+    // the kernels number their tiles in 32 bits
+    if (((__int128)(D.M + 15) / 16) * ((D.N + 127) / 128) * D.batch >= (1ll << 31))
+        return FP8BQ_ERR_SHAPE;
     const int es = esize_of(D.dtype_out);
     const int64_t obs = D.batch > 1 ? D.out_batch_stride : 0;
     if (obs < 0) return FP8BQ_ERR_SHAPE;
@@ -320,10 +323,6 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     if (overlap) return FP8BQ_ERR_OVERLAP;
     const fp8bq_status sd = device_status();
     if (sd != FP8BQ_OK) return sd;
-
-    // the kernels number their tiles in 32 bits
-    if (((__int128)(D.M + 15) / 16) * ((D.N + 127) / 128) * D.batch >= (1ll << 31))
-        return FP8BQ_ERR_SHAPE;
 
     const int64_t kb = fp4_row_bytes(D.K), stages = (kb + 127) / 128;
     const int tokens = fp4_choose(D.M, D.N, stages, D.batch, gated);

@@ -335,8 +335,12 @@ typedef struct fp8bq_fp4_operand {
  *         out[e] behind them are left as they were.  Read on the stream.
  *
  * K >= 1 (FP8BQ_ERR_SHAPE otherwise: an empty sum is refused).  Empty M, N or
- * batch: nothing is done.  batch and ceil(M / 128) at most 65535.  out must
- * overlap no input, and its matrices not each other.
+ * batch: nothing is done.  batch * ceil(M / 16) * ceil(N / 128) below 2^31.  out
+ * must overlap no input, and its matrices not each other.
+ *
+ * A wait inside a kernel that runs out is reported by fp8bq_sync_status, as for
+ * the quantizer's TMA kernel; fp8bq_debug_set_wait_limit_ns and
+ * FP8BQ_INJECT_DROP_FIRST_LOAD act on these kernels too.
  */
 typedef struct fp8bq_fp4_matmul_desc {
     fp8bq_fp4_operand a, b, up; /* up: fp8bq_fp4_gated_matmul only */

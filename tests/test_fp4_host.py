@@ -95,8 +95,8 @@ def mm(**kw):
     (dict(K=0), fq.FP8BQ_ERR_SHAPE),
     (dict(M=-1), fq.FP8BQ_ERR_SHAPE),
     (dict(N=-5), fq.FP8BQ_ERR_SHAPE),
-    (dict(batch=65536), fq.FP8BQ_ERR_SHAPE),
-    (dict(M=65535 * 128 + 1), fq.FP8BQ_ERR_SHAPE),
+    (dict(batch=1 << 30, M=128, N=1, ld_out=1, out_batch_stride=128), fq.FP8BQ_ERR_SHAPE),
+    (dict(M=(1 << 31) - 255, ld_out=256, out_batch_stride=1 << 40), fq.FP8BQ_ERR_SHAPE),
     (dict(ld_out=255), fq.FP8BQ_ERR_SHAPE),
     (dict(a__codes_batch_stride=-16), fq.FP8BQ_ERR_SHAPE),
     (dict(b__scales_batch_stride=1 << 40), fq.FP8BQ_ERR_SHAPE),

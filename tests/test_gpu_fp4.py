@@ -229,6 +229,28 @@ def test_product_is_exact_where_its_sums_are(M, N, K, fmt, out):
     assert torch.equal(y, fq.matmul_fp4(a, sa, b, sb, fmt, out_dtype=out))
 
 
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", [(1, 77, 2048), (9, 400, 64), (40, 129, 512), (100, 1030, 256),
+                                   (200, 131, 1024), (40, 40000, 32), (700, 515, 64)])
+def test_outputs_of_every_alignment(M, N, K, out):
+    """Row strides and starts that allow 32-, 16-, 8-, 4-byte stores or the element's only; nothing
+    beside the output is written."""
+    a, sa, va = exact_operand(M, K, 1, "mxfp4")
+    b, sb, vb = exact_operand(N, K, 2, "mxfp4")
+    want = rounded(va @ vb.T, out)
+    es = 2 if out == torch.bfloat16 else 4
+    for ld, start in ((N + -N % 16, 0), (N + -N % 16 + 8, 0), (N + -N % 4 + 4, 0), (N + -N % 2 + 2, 2),
+                      (N, 0), (N + 1 - N % 2, 1)):
+        buf = Guarded((M * ld + start) * es)
+        flat = buf.view.view(out)
+        y = flat.as_strided((M, N), (ld, 1), flat.storage_offset() + start)
+        fq.matmul_fp4(a, sa, b, sb, "mxfp4", out=y)
+        assert np.array_equal(as_float(y), want), (ld, start)
+        assert buf.canaries_intact()
+        rows = buf.view[start * es:].view(M, ld, es)
+        assert (rows[:, N:] == CANARY).all() and (buf.view[:start * es] == CANARY).all()
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("M,N,K,E", [(2300, 5000, 288, 0), (700, 1100, 1600, 9), (16500, 330, 96, 0)])
 def test_products_of_many_tiles(fmt, M, N, K, E):
@@ -490,6 +512,9 @@ def test_conveniences_refuse_what_does_not_fit():
     bad = [
         (ValueError, lambda: fq.scaled_fp4_blockwise(x.t(), "mxfp4")),          # strided columns
         (ValueError, lambda: fq.scaled_fp4_blockwise(x[0], "mxfp4")),
+        (ValueError, lambda: fq.scaled_fp4_blockwise(x[:1].expand(40, 96), "mxfp4")),   # rows overlap
+        (ValueError, lambda: fq.matmul_fp4(c, s, c, s, out=torch.empty(1, 40, device="cuda").expand(
+            40, 40))),
         (TypeError, lambda: fq.scaled_fp4_blockwise(x.half(), "mxfp4")),
         (ValueError, lambda: fq.scaled_fp4_blockwise(x, "mxfp4", tensor_scale=t)),
         (TypeError, lambda: fq.scaled_fp4_blockwise(x, "nvfp4", tensor_scale=t.double())),
@@ -533,3 +558,26 @@ def test_empty_inputs():
     assert fq.matmul_fp4(c, s, w, ws).shape == (0, 16)
     assert fq.matmul_fp4(w, ws, c, s).shape == (16, 0)
     assert fq.quant_weights_fp4([]) == []
+
+
+def test_offsets_beyond_32_bits():
+    """A weight whose codes, and a product whose outputs, pass 4 GiB: the last rows are right."""
+    M, K = 600_000, 16384                                     # 19.7 GB of bf16, 4.9 GB of codes
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(300, K, device="cuda").to(torch.bfloat16)
+    x[-300:] = tail
+    c, s = fq.scaled_fp4_blockwise(x)
+    del x
+    ct, st = fq.scaled_fp4_blockwise(torch.cat([torch.zeros(M % 128 + 128 * 3 - 300, K, device="cuda",
+                                                            dtype=torch.bfloat16), tail]))
+    assert torch.equal(c[-300:], ct[-300:]) and not c[:-300].any()
+    assert torch.equal(s[-3:], st[-3:])
+    v = fq.dequantize_fp4_blockwise(c, s, out_dtype=torch.bfloat16)
+    assert torch.equal(v[-300:], fq.dequantize_fp4_blockwise(ct, st)[-300:])
+    del v
+    w, ws = fq.scaled_fp4_blockwise(torch.randn(4000, K, device="cuda").to(torch.bfloat16))
+    y = fq.matmul_fp4(c, s, w, ws)                            # 600,000 x 4000 bf16: 4.8 GB
+    yt = fq.matmul_fp4(ct, st, w, ws)
+    assert torch.equal(y[-300:], yt[-300:]) and not y[:-300].any()
+    y1 = fq.matmul_fp4(w[:7], ws[:1], c, s)                   # 600,000 outputs of 7 tokens
+    assert torch.equal(y1[:, -300:].t(), y[-300:, :7])
