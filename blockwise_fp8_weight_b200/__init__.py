@@ -602,13 +602,55 @@ def quant_weights(weights: Iterable, weight_block_size=DEFAULT_BLOCK, stream=Non
 # ----------------------------------------------------------------- 4-bit conveniences
 #
 # A product of one token takes the GPU a few microseconds, so what these
-# functions do on the host is most of such a call: the descriptor is packed in
-# one call of the struct module, and the checks look at each property once.
+# functions do on the host is most of such a call.  The ordinary call (contiguous
+# CUDA tensors that fit each other, on the current stream) is made by the module
+# `_calls` (csrc/fp8bq_calls.c), which returns None for any other; the code here
+# then takes it, checks it and says what is wrong with it.
 
 _FP4_FORMATS = {"mxfp4": (FP8BQ_MXFP4, 32), "nvfp4": (FP8BQ_NVFP4, 16)}
 # fp8bq_fp4_desc and fp8bq_fp4_matmul_desc as packed bytes
 _FP4_DESC = struct.Struct("<4Q6q2i")
 _FP4_MATMUL_DESC = struct.Struct("<" + 3 * "3Q3q" + "2Q6q2i")
+
+
+_calls = None
+
+
+def _load_calls():
+    """The call module, built if it is missing or older than its source."""
+    global _calls
+    L = lib()
+    with _lock:
+        if _calls is None:
+            import importlib.machinery
+            import importlib.util
+
+            import torch
+
+            from . import build as _build
+            spec = importlib.util.spec_from_file_location(__name__ + "._calls", _build.build_calls())
+            m = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(m)
+            m.setup(torch.Tensor, torch.uint8, torch.bfloat16, torch.float32,
+                    *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                        L.fp8bq_fp4_matmul, L.fp8bq_fp4_gated_matmul, L.fp8bq_fp4_quantize_batched,
+                        L.fp8bq_fp4_dequantize)))
+            _calls = m
+    return _calls
+
+
+def _fp4_quick(name: str, what: str, like, format: str, lead, args):
+    """The call by the call module, or None where it is not an ordinary one."""
+    f = _FP4_FORMATS.get(format) if type(format) is str else None
+    if f is None or not getattr(like, "is_cuda", False):
+        return None
+    import torch
+    dev = torch._C._cuda_getDevice()
+    r = getattr(_calls or _load_calls(), name)(
+        *lead, f[0], dev, torch._C._cuda_getCurrentRawStream(dev), *args)
+    if type(r) is int:
+        check(r, what)
+    return r
 
 
 def _fp4_format(format: str) -> tuple[int, int]:
@@ -691,6 +733,11 @@ def scaled_fp4_blockwise(data_hp, format="mxfp4", tensor_scale=None, stream=None
     the block length, in the tiles that the products read (``fp4_scale_rows``
     gives them row by row).  Both are padded with zeros.
     """
+    if stream is None:
+        r = _fp4_quick("quantize", "scaled_fp4_blockwise", data_hp, format, (),
+                       (data_hp, tensor_scale))
+        if r is not None:
+            return r
     _, block = _fp4_format(format)
     torch, _, current, L = _fp4_setup(data_hp, "data_hp")
     cs, ss, rec = _fp4_record(data_hp, "data_hp", format, block, tensor_scale)
@@ -790,6 +837,11 @@ def dequantize_fp4_blockwise(codes, scales, format="mxfp4", columns=None, tensor
                              out_dtype=None, stream=None):
     """Reverse map of ``scaled_fp4_blockwise``: the values as bf16 (default) or
     fp32, [(E,) M, columns] (default: every column the codes have room for)."""
+    if stream is None:
+        r = _fp4_quick("dequantize", "dequantize_fp4_blockwise", codes, format, (),
+                       (codes, scales, tensor_scale, columns, out_dtype))
+        if r is not None:
+            return r
     fmt, block = _fp4_format(format)
     torch, dev, current, L = _fp4_setup(codes, "codes")
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
@@ -873,6 +925,12 @@ def matmul_fp4(a, a_scales, b, b_scales, format="mxfp4", a_tensor_scale=None, b_
 
     The codes carry no gradient: they are what an inference engine holds.
     """
+    if stream is None and rows is None and out is None:
+        r = _fp4_quick("product", "matmul_fp4", a, format, (0,),
+                       (a, a_scales, a_tensor_scale, b, b_scales, b_tensor_scale, None, None, None,
+                        out_dtype))
+        if r is not None:
+            return r
     return _fp4_product("matmul", (a, a_scales, a_tensor_scale), (b, b_scales, b_tensor_scale),
                         None, format, out_dtype, rows, out, stream)
 
@@ -884,6 +942,12 @@ def gated_matmul_fp4(a, a_scales, gate, gate_scales, up, up_scales, format="mxfp
     kernel; operands and arguments as in ``matmul_fp4``.  The halves of a fused
     [(E,) 2F, K] weight may be views of it where F is a multiple of 128
     (codes[..., :F, :], scales[..., :F // 128, :, :, :], and the rest)."""
+    if stream is None and rows is None and out is None:
+        r = _fp4_quick("product", "gated_matmul_fp4", a, format, (1,),
+                       (a, a_scales, a_tensor_scale, gate, gate_scales, gate_tensor_scale, up,
+                        up_scales, up_tensor_scale, out_dtype))
+        if r is not None:
+            return r
     return _fp4_product("gated_matmul", (a, a_scales, a_tensor_scale),
                         (gate, gate_scales, gate_tensor_scale), (up, up_scales, up_tensor_scale),
                         format, out_dtype, rows, out, stream)

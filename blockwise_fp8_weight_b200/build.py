@@ -15,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,6 +28,9 @@ HEADERS = [os.path.join(CSRC, f) for f in ("fp8bq_internal.h", "fp8bq_device.cuh
                                                    "fp8bq_tile.cuh", "fp8bq_fp4.h",
                                                    "fp8bq_fp4_device.cuh")] + [
     os.path.join(ROOT, "include", "fp8bq.h")]
+# the Python binding's call module (C, no CUDA code of its own)
+CALLS_SOURCE = os.path.join(CSRC, "fp8bq_calls.c")
+CALLS = os.path.join(PKG, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 LIB = os.path.join(PKG, "libfp8bq.so")
 LIB_CHECKED = os.path.join(PKG, "libfp8bq_checked.so")
 
@@ -51,12 +55,29 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(f) <= t for f in SOURCES + HEADERS)
 
 
+def build_calls(force: bool = False) -> str:
+    """Compile the binding's call module with the C compiler; returns its path."""
+    deps = (CALLS_SOURCE, os.path.join(ROOT, "include", "fp8bq.h"))
+    if not force and os.path.exists(CALLS) and \
+            all(os.path.getmtime(f) <= os.path.getmtime(CALLS) for f in deps):
+        return CALLS
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = CALLS + f".tmp{os.getpid()}"
+    subprocess.run([os.environ.get("CC", "gcc"), "-O2", "-std=c11", "-Wall", "-Wextra", "-fPIC",
+                    "-shared", "-I", os.path.join(ROOT, "include"), "-I", cuda,
+                    "-I", sysconfig.get_paths()["include"], "-o", tmp, CALLS_SOURCE], check=True)
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, out: str | None = None,
           defines: tuple[str, ...] = (), checked: bool = False) -> str:
     """Compile the library (to ``out``, default the in-tree path); ``defines``
     are extra -D tuning constants; ``checked`` builds the bounds-checked
     library (default path ``libfp8bq_checked.so``)."""
     lib = out or (LIB_CHECKED if checked else LIB)
+    if out is None:
+        build_calls(force)
     if checked:
         defines = (*defines, "FP8BQ_CHECKED=1")
     if out is None and not force and not verbose_ptxas and \

@@ -17,12 +17,12 @@ uint32_t inject_flags();            // FP8BQ_INJECT_*
 uint64_t checked_extent(uint64_t);  // an output's extent for the bounds checks
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
-// Whether a call of this much work is launched with programmatic stream
-// serialization.  The attribute costs the host 1.6 us a launch (4.2 against
-// 2.6 on the pool's hosts), more than the overlap saves where the host is the
-// slower side: calls that take the device less than a few microseconds,
-// outside a graph.
-bool fp4_overlap(cudaStream_t st, double bytes, double flops);
+// Whether a call that takes the device about `us` microseconds is launched
+// with programmatic stream serialization.  The attribute costs the host 1.6 us
+// a launch (4.2 against 2.6 on the pool's hosts), and saves the device 2 to 3:
+// it is left out where the host, at about 9 us a call through the Python
+// binding, is the slower side of the two anyway, outside a graph.
+bool fp4_overlap(cudaStream_t st, double us);
 
 // ------------------------------------------------------------------ layout
 //
@@ -108,7 +108,7 @@ struct Fp4MmParams {
 cudaError_t launch_fp4_mm_narrow(const Fp4MmParams &p, int format, bool gated, bool out_bf16,
                                  int tokens, cudaStream_t st);
 // Which kernel: 0 the one for many tokens, else the tile's width in tokens.
-int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated);
+int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated, double *us);
 // Tiles of 256 tokens by 256 outputs (gated: 128) on pairs of SMs.
 cudaError_t launch_fp4_mm_wide(const Fp4MmParams &p, int format, bool gated, bool out_bf16,
                                cudaStream_t st);

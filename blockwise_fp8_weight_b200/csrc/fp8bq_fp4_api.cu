@@ -10,9 +10,9 @@
 
 using namespace fp8bq;
 
-bool fp8bq::fp4_overlap(cudaStream_t st, double bytes, double flops) {
+bool fp8bq::fp4_overlap(cudaStream_t st, double us) {
     if (!pdl_enabled()) return false;
-    if (bytes / 6.5e12 + flops / 3.5e15 > 8e-6) return true;
+    if (us > 8.5) return true;
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) {
         cudaGetLastError();
@@ -171,7 +171,7 @@ fp8bq_status run_quantize(std::vector<Stack> &t, cudaStream_t stream) {
     if (overlaps(ranges)) return FP8BQ_ERR_OVERLAP;
     const fp8bq_status sd = device_status();
     if (sd != FP8BQ_OK) return sd;
-    const bool overlap = fp4_overlap(stream, bytes, 0);
+    const bool overlap = fp4_overlap(stream, 2 + bytes * 1.6e-7);
     for (auto &by_format : groups)
         for (auto &by_type : by_format)
             for (int a = 0; a < 4; ++a) {
@@ -212,7 +212,8 @@ fp8bq_status run_dequantize(Stack D, cudaStream_t stream) {
     fill(D, true, 0, &p.d[0]);
     p.total = p.d[0].items;
     const int es = esize_of(D.dtype);
-    const bool overlap = fp4_overlap(stream, (double)D.batch * D.M * D.K * (es + 0.5), 0);
+    const bool overlap =
+        fp4_overlap(stream, 2 + (double)D.batch * D.M * D.K * (es + 0.5) * 1.6e-7);
     if (launch_fp4_dequantize<kMaxDescSmall>(p, D.format, es, align_of(D), overlap, stream) !=
         cudaSuccess) {
         cudaGetLastError();
@@ -325,7 +326,8 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     if (sd != FP8BQ_OK) return sd;
 
     const int64_t kb = fp4_row_bytes(D.K), stages = (kb + 127) / 128;
-    const int tokens = fp4_choose(D.M, D.N, stages, D.batch, gated);
+    double us = 0;
+    const int tokens = fp4_choose(D.M, D.N, stages, D.batch, gated, &us);
     const bool wide = tokens == 0;
     Fp4MmParams p;
     std::memset(&p, 0, sizeof p);
@@ -356,8 +358,7 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
             p.store_align = a;
     for (int i = 0; i < n; ++i)  // a stack stride of 0: one matrix for the whole stack
         p.moves |= (mats[i].cbs ? 1u : 0u) << (2 * i) | (mats[i].sbs ? 2u : 0u) << (2 * i);
-    const double weights = (double)(n - 1) * D.batch * D.N * D.K;
-    p.overlap = fp4_overlap(stream, 0.5 * weights + (double)out_bytes, 2.0 * weights * D.M);
+    p.overlap = fp4_overlap(stream, us);
     p.inject = inject_flags();
 #if FP8BQ_CHECKED
     p.out_bytes = checked_extent((uint64_t)out_bytes);

@@ -1034,12 +1034,13 @@ cudaError_t launch_fp4_mm_wide(const Fp4MmParams &p, int format, bool gated, boo
                                  : wide_format<FP8BQ_NVFP4>(p, gated, out_bf16, st);
 }
 
-// The kernel for a product: the tile's width in tokens of the few-token kernel,
-// or 0 for the many-token one.  Up to 32 tokens the narrowest tile that holds
-// them; beyond, the one with the shortest estimate.  A call takes about
+// The kernel for a product, and what it takes about: the tile's width in
+// tokens of the few-token kernel, or 0 for the many-token one.  Up to 32 tokens
+// the narrowest tile that holds them; beyond, the one with the shortest
+// estimate.  A call takes about
 //     begin + stage * (stages of a CTA) + again * (stages) * (rounds - 1)
 // microseconds, rounds = tiles over the tiles that run at once.  Fitted to
-// B200, 1000 x 4100 to 12288 x 4096 and 4096 x 12288, 64 to 2048 tokens, mxfp4
+// B200, 1000 x 4100 to 12288 x 4096 and 4096 x 12288, 1 to 2048 tokens, mxfp4
 // (measured, us, many-token / 64 / 128 / 256 wide tiles):
 //     515 tokens, 1000 x 4100    13.7 / 10.7 /  9.8 / 11.5
 //     256 tokens, 4096 x 4096    12.2 / 10.7 / 10.2 / 10.9
@@ -1048,24 +1049,26 @@ cudaError_t launch_fp4_mm_wide(const Fp4MmParams &p, int format, bool gated, boo
 //     1024 tokens, 6144 x 4096   20.5 / 29.1 / 27.6 / 30.3
 //     gated, 256 x 4096 x 4096   12.8 / 15.0 / 13.4
 //     gated, 64 x 12288 x 4096   21.3 / 15.8 / 15.9
-int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated) {
-    if (M <= 16) return 16;
-    if (M <= 32) return 32;
+int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated, double *us) {
     struct Cost {
         int tokens;
         double begin, stage, again;
     };
-    static constexpr Cost plain[] = {
-        {0, 4.8, 0.45, 0.50}, {64, 6.2, 0.40, 0.45}, {128, 7.0, 0.36, 0.47}, {256, 8.6, 0.50, 0.90}};
-    static constexpr Cost both[] = {{0, 4.8, 0.47, 0.50}, {64, 8.3, 0.42, 0.57}, {128, 9.5, 0.55, 0.85}};
+    static constexpr Cost plain[] = {{16, 4.9, 0.33, 0.40}, {32, 5.3, 0.33, 0.42},
+                                     {0, 4.8, 0.45, 0.50},  {64, 6.2, 0.40, 0.45},
+                                     {128, 7.0, 0.36, 0.47}, {256, 8.6, 0.50, 0.90}};
+    static constexpr Cost both[] = {{16, 5.5, 0.45, 0.60}, {32, 6.5, 0.45, 0.60},
+                                    {0, 4.8, 0.47, 0.50},  {64, 8.3, 0.42, 0.57},
+                                    {128, 9.5, 0.55, 0.85}};
     const double sms = sm_count();
+    const int first = M <= 16 ? 0 : M <= 32 ? 1 : 2, last = M <= 32 ? first : gated ? 4 : 5;
     int best = 0;
-    double least = 0;
-    for (int i = 0; i < (gated ? 3 : 4); ++i) {
+    for (int i = first; i <= last; ++i) {
         const Cost &c = gated ? both[i] : plain[i];
         const int64_t rows = c.tokens ? c.tokens : 256, cols = c.tokens || gated ? 128 : 256;
         const double tiles = (double)((M + rows - 1) / rows) * (double)((N + cols - 1) / cols) * batch;
-        const double once = c.tokens == 0 ? sms / 2 : c.tokens == 64 && !gated ? 2 * sms : sms;
+        const bool two = c.tokens && c.tokens <= (gated ? 16 : 64);  // CTAs an SM
+        const double once = c.tokens == 0 ? sms / 2 : two ? 2 * sms : sms;
         double share = (double)stages;  // stages of a CTA where a cluster splits K
         if (c.tokens)
             for (int s : {2, 3, 4, 6, 8})  // clusters of more than two leave some SMs out
@@ -1073,8 +1076,8 @@ int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated) 
                     share = (double)((stages + s - 1) / s);
         const double rounds = (double)(int64_t)((tiles + once - 1) / once);
         const double t = c.begin + c.stage * share + c.again * stages * (rounds - 1);
-        if (i == 0 || t < least) {
-            least = t;
+        if (i == first || t < *us) {
+            *us = t;
             best = c.tokens;
         }
     }

@@ -206,3 +206,23 @@ def test_reference_scales_and_error_bound():
     t = np.float32(np.abs(x).max() / 2688)
     _, sc = ref.quantize(x, "nvfp4", t)
     assert sc.max() == 126                       # 448: the largest block's scale
+
+
+def test_the_call_module_leaves_what_is_not_ordinary():
+    """It returns None, with nothing done and no Python error pending, for anything but contiguous
+    CUDA tensors that fit each other; the conveniences then say what is wrong."""
+    m = fq._load_calls()
+    x = torch.zeros(4, 64)
+    c, s = torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(1, 1, 32, 16, dtype=torch.uint8)
+    for call in (lambda: m.product(0, 0, 0, 0, c, s, None, c, s, None, None, None, None, None),
+                 lambda: m.product(0, 0, -1, 0, c, s, None, c, s, None, None, None, None, None),
+                 lambda: m.product(1, 0, 0, 0, 1, "a", None, [], s, None, None, None, None, None),
+                 lambda: m.product(0, "x", 0, 0, c, s, None, c, s, None, None, None, None, None),
+                 lambda: m.product(0, 0, 0), lambda: m.product(),
+                 lambda: m.quantize(0, 0, 0, x, None), lambda: m.quantize(0, 0, 0, None, None),
+                 lambda: m.quantize(0, 0, 1 << 80, x, None), lambda: m.quantize(),
+                 lambda: m.dequantize(0, 0, 0, c, s, None, None, None),
+                 lambda: m.dequantize(0, -1, 0, c, s, None, None, None), lambda: m.dequantize(1)):
+        assert call() is None
+    with pytest.raises(TypeError):
+        m.setup(1, 2, 3)

@@ -581,3 +581,37 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(y[-300:], yt[-300:]) and not y[:-300].any()
     y1 = fq.matmul_fp4(w[:7], ws[:1], c, s)                   # 600,000 outputs of 7 tokens
     assert torch.equal(y1[:, -300:].t(), y[-300:, :7])
+
+
+def test_the_call_module_and_the_python_path_agree(monkeypatch):
+    """The ordinary call goes through the call module; a stream, rows or an output given goes
+    through Python: the same outputs."""
+    now = torch.cuda.current_stream()
+    t = torch.tensor([0.01], device="cuda")
+    for fmt in FORMATS:
+        ts = t if fmt == "nvfp4" else None
+        for shape in ((3, 100), (2, 40, 96)):
+            for dtype in (torch.bfloat16, torch.float32):
+                x = torch.randn(shape, device="cuda").to(dtype)
+                quick, slow = (fq.scaled_fp4_blockwise(x, fmt, ts, **k) for k in ({}, {"stream": now}))
+                assert all(torch.equal(a, b) for a, b in zip(quick, slow))
+                for k in (dict(columns=shape[-1]), dict(out_dtype=torch.float32), dict()):
+                    a, b = (fq.dequantize_fp4_blockwise(*quick, fmt, tensor_scale=ts, **k, **e)
+                            for e in ({}, {"stream": now}))
+                    assert a.dtype == b.dtype and torch.equal(a, b)
+                for out in (None, torch.float32):
+                    a, b = (fq.matmul_fp4(*quick, *quick, fmt, ts, ts, out_dtype=out, **e)
+                            for e in ({}, {"stream": now}))
+                    assert a.dtype == b.dtype and torch.equal(a, b)
+                    a, b = (fq.gated_matmul_fp4(*quick, *quick, *quick, fmt, ts, ts, ts, out_dtype=out,
+                                                **e) for e in ({}, {"stream": now}))
+                    assert a.dtype == b.dtype and torch.equal(a, b)
+    w = torch.nn.Parameter(torch.randn(5, 64, device="cuda"))     # a subclass of Tensor
+    assert torch.equal(fq.scaled_fp4_blockwise(w)[0], fq.scaled_fp4_blockwise(w.detach())[0])
+    with monkeypatch.context() as m:
+        m.setattr(fq, "_fp4_product", None)
+        m.setattr(fq, "_fp4_setup", None)
+        c, s = fq.scaled_fp4_blockwise(x[0], "mxfp4")
+        fq.dequantize_fp4_blockwise(c, s)
+        fq.matmul_fp4(c, s, c, s)
+        fq.gated_matmul_fp4(c, s, c, s, c, s)
