@@ -1038,9 +1038,11 @@ cudaError_t launch_fp4_mm_wide(const Fp4MmParams &p, int format, bool gated, boo
 // tokens of the few-token kernel, or 0 for the many-token one.  Up to 32 tokens
 // the narrowest tile that holds them; beyond, the one with the shortest
 // estimate.  A call takes about
-//     begin + stage * (stages of a CTA) + again * (stages) * (rounds - 1)
-// microseconds, rounds = tiles over the tiles that run at once.  Fitted to
-// B200, 1000 x 4100 to 12288 x 4096 and 4096 x 12288, 1 to 2048 tokens, mxfp4
+//     begin + stage * (stages of a CTA)
+//           + max(again * (stages), round) * (rounds - 1)
+// microseconds, rounds = tiles over the tiles that run at once; `round` is the
+// time to store a tile.  Fitted to B200, 1000 x 4100 to 12288 x 4096 and 4096 x
+// 12288, stacks of 8 to 128 of 768 x 2048 to 4096 x 4096, 1 to 2048 tokens, mxfp4
 // (measured, us, many-token / 64 / 128 / 256 wide tiles):
 //     515 tokens, 1000 x 4100    13.7 / 10.7 /  9.8 / 11.5
 //     256 tokens, 4096 x 4096    12.2 / 10.7 / 10.2 / 10.9
@@ -1049,17 +1051,19 @@ cudaError_t launch_fp4_mm_wide(const Fp4MmParams &p, int format, bool gated, boo
 //     1024 tokens, 6144 x 4096   20.5 / 29.1 / 27.6 / 30.3
 //     gated, 256 x 4096 x 4096   12.8 / 15.0 / 13.4
 //     gated, 64 x 12288 x 4096   21.3 / 15.8 / 15.9
+//     128 of 128 x 2048 x 768    41.4 / 46.0 / 61.4 / 71.2
+//     128 of 64 x 2048 x 768     32.1 / 26.3 / 36.9 / 46.5
 int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated, double *us) {
     struct Cost {
         int tokens;
-        double begin, stage, again;
+        double begin, stage, again, round;
     };
-    static constexpr Cost plain[] = {{16, 4.9, 0.33, 0.40}, {32, 5.3, 0.33, 0.42},
-                                     {0, 4.8, 0.45, 0.50},  {64, 6.2, 0.40, 0.45},
-                                     {128, 7.0, 0.36, 0.47}, {256, 8.6, 0.50, 0.90}};
-    static constexpr Cost both[] = {{16, 5.5, 0.45, 0.60}, {32, 6.5, 0.45, 0.60},
-                                    {0, 4.8, 0.47, 0.50},  {64, 8.3, 0.42, 0.57},
-                                    {128, 9.5, 0.55, 0.85}};
+    static constexpr Cost plain[] = {{16, 4.9, 0.33, 0.40, 2.5}, {32, 5.3, 0.33, 0.42, 2.5},
+                                     {0, 4.8, 0.45, 0.50, 2.6},  {64, 6.2, 0.40, 0.45, 2.8},
+                                     {128, 7.0, 0.36, 0.55, 3.9}, {256, 8.6, 0.50, 0.90, 4.5}};
+    static constexpr Cost both[] = {{16, 5.5, 0.45, 0.60, 2.6}, {32, 6.5, 0.45, 0.60, 2.6},
+                                    {0, 4.8, 0.47, 0.55, 2.8},  {64, 8.3, 0.42, 0.57, 2.8},
+                                    {128, 9.5, 0.55, 1.00, 5.8}};
     const double sms = sm_count();
     const int first = M <= 16 ? 0 : M <= 32 ? 1 : 2, last = M <= 32 ? first : gated ? 4 : 5;
     int best = 0;
@@ -1075,7 +1079,8 @@ int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated, 
                 if (s <= stages && tiles * s <= once * (s == 2 ? 1.0 : s == 8 ? 0.82 : 0.9))
                     share = (double)((stages + s - 1) / s);
         const double rounds = (double)(int64_t)((tiles + once - 1) / once);
-        const double t = c.begin + c.stage * share + c.again * stages * (rounds - 1);
+        const double again = c.again * stages > c.round ? c.again * stages : c.round;
+        const double t = c.begin + c.stage * share + again * (rounds - 1);
         if (i == first || t < *us) {
             *us = t;
             best = c.tokens;
