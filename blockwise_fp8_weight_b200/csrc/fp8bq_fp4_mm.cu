@@ -957,7 +957,10 @@ ClusterFit cluster_fit(K kern, unsigned threads, int smem, int per_sm) {
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        f.attr = cudaOccupancyMaxActiveClusters(&f.n[c], kern, &cfg);
+        if (cudaOccupancyMaxActiveClusters(&f.n[c], kern, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            f.n[c] = 0;
+        }
         f.n[c] *= per_sm;
     }
     if (f.attr == cudaSuccess && f.n[1] < 1) f.attr = cudaErrorInvalidConfiguration;
