@@ -19,7 +19,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Whether a call that takes the device about `us` microseconds is launched
 // with programmatic stream serialization.  The attribute costs the host 1.6 us
-// a launch (4.2 against 2.6 on the pool's hosts), and saves the device 2 to 3:
+// a launch (4.2 against 2.6 measured), and saves the device 2 to 3:
 // it is left out where the host, at about 9 us a call through the Python
 // binding, is the slower side of the two anyway, outside a graph.
 bool fp4_overlap(cudaStream_t st, double us);

@@ -1,4 +1,8 @@
 """The 4-bit operators on the GPU against their formulas in 64 bits."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -615,3 +619,81 @@ def test_the_call_module_and_the_python_path_agree(monkeypatch):
         fq.dequantize_fp4_blockwise(c, s)
         fq.matmul_fp4(c, s, c, s)
         fq.gated_matmul_fp4(c, s, c, s, c, s)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M", [5, 60, 600])
+def test_no_valid_rows_at_all(M, gated):
+    E, N, K = 3, 300, 512
+    a, sa, _, g, sg, _, u, su, _ = gated_operands(M, N, K, "mxfp4", E)
+    rows = torch.zeros(E, dtype=torch.int32, device="cuda")
+    out = torch.full((E, M, N), 7.0, device="cuda")
+    if gated:
+        fq.gated_matmul_fp4(a, sa, g, sg, u, su, rows=rows, out=out)
+    else:
+        fq.matmul_fp4(a, sa, g, sg, rows=rows, out=out)
+    assert (out == 7.0).all()
+
+
+def test_a_long_list_of_weights():
+    """More weights of one kind than one launch's descriptors hold."""
+    g = torch.Generator().manual_seed(5)
+    named = [(f"w{i}", torch.randn(1 + i % 7, 1 + (i * 13) % 90, generator=g).cuda()) for i in range(700)]
+    named += [(f"s{i}", torch.randn(2, 3, 64, generator=g).cuda().to(torch.bfloat16)) for i in range(9)]
+    out = dict(fq.quant_weights_fp4(named, "mxfp4"))
+    for name, w in named:
+        c, s = fq.scaled_fp4_blockwise(w, "mxfp4")
+        assert torch.equal(out[name], c) and torch.equal(out[name + "_scale"], s)
+
+
+FIRST_CALL = """
+import torch, blockwise_fp8_weight_b200 as fq
+x = torch.randn(%d, 512, device="cuda")
+w = torch.randn(300, 512, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    c, s = fq.scaled_fp4_blockwise(x)
+    d, t = fq.scaled_fp4_blockwise(w)
+    y = fq.matmul_fp4(c, s, d, t)
+    h = fq.gated_matmul_fp4(c, s, d, t, d, t)
+    v = fq.dequantize_fp4_blockwise(c, s)
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(y, fq.matmul_fp4(c, s, d, t))
+assert torch.equal(h, fq.gated_matmul_fp4(c, s, d, t, d, t))
+assert torch.equal(v, fq.dequantize_fp4_blockwise(*fq.scaled_fp4_blockwise(x)))
+assert fq.fp8bq_sync_status() == fq.FP8BQ_OK
+"""
+
+
+@pytest.mark.parametrize("M", [2, 700])
+def test_the_first_call_of_a_process_may_be_captured(M):
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL % M], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-3000:]
+
+
+def test_calls_from_several_host_threads():
+    import threading
+    a, sa, va = exact_operand(20, 512, 1, "mxfp4")
+    b, sb, vb = exact_operand(400, 512, 2, "mxfp4")
+    want = torch.from_numpy(va @ vb.T).cuda().float()
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(50):
+                    if not torch.equal(fq.matmul_fp4(a, sa, b, sb, out_dtype=torch.float32), want):
+                        bad.append("differs")
+        except Exception as e:  # noqa: BLE001 -- reported by the test
+            bad.append(e)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad[:3]
