@@ -829,7 +829,7 @@ def _fp4_operand(torch, dev, codes, scales, tensor_scale, format: str, block: in
             raise ValueError(f"{what}: the scale tiles must be contiguous")
         cbs, sbs = cs[0], st[0]
     t, ts = (0, 0) if tensor_scale is None else \
-        _fp4_tensor_scale(tensor_scale, max(E, 1), format, f"{what}'s tensor scale")
+        _fp4_tensor_scale(tensor_scale, E if dim == 3 else 1, format, f"{what}'s tensor scale")
     return codes.data_ptr(), scales.data_ptr(), t, cbs, sbs, ts, E, rows, kb, dim
 
 

@@ -551,6 +551,19 @@ def test_conveniences_refuse_what_does_not_fit():
             pytest.fail(f"call {i} was not refused")
 
 
+def test_empty_stacks_with_a_scale_for_each_matrix():
+    x = torch.empty(0, 130, 96, device="cuda")
+    t = torch.empty(0, device="cuda")
+    c, s = fq.scaled_fp4_blockwise(x, "nvfp4", t)
+    assert fq.dequantize_fp4_blockwise(c, s, "nvfp4", tensor_scale=t).shape == x.shape
+    for ts in (t, torch.ones(1, device="cuda"), None):
+        assert fq.matmul_fp4(c, s, c, s, "nvfp4", ts, ts).shape == (0, 130, 130)
+        assert fq.gated_matmul_fp4(c, s, c, s, c, s, "nvfp4", ts, ts, ts).shape == (0, 130, 130)
+    c, s = fq.scaled_fp4_blockwise(torch.ones(2, 96, device="cuda"), "nvfp4")
+    with pytest.raises(ValueError):
+        fq.matmul_fp4(c, s, c, s, "nvfp4", t)
+
+
 def test_empty_inputs():
     for shape in ((0, 64), (3, 0), (0, 5, 64), (2, 0, 64)):
         x = torch.zeros(shape, device="cuda")
