@@ -22,7 +22,7 @@ constexpr uint64_t kDrainNs = 2000000000ull;
 // v / (1 + exp(-v)) by the fast exponential and division: their documented
 // errors are 2 + |1.173 v| and 2 units in the last place, far below the
 // rounding of a bf16 output and of the order of an fp32 sum's own.  (expf and
-// the IEEE division: 313 us instead of 62 for 8192 x 6144 outputs over
+// the IEEE division: 313 us instead of 60 for 8192 x 6144 outputs over
 // K = 512, on B200.)
 __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
 
@@ -564,9 +564,9 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
 // first, and the next tile waits for those alone.  The scales' buffers take
 // the last 96 columns.
 //
-// Measured on B200, 8192 tokens against 6144 x 4096 (mxfp4 / nvfp4): 107 / 110 us;
+// Measured on B200, 8192 tokens against 6144 x 4096 (mxfp4 / nvfp4): 92 / 103 us;
 // with the scales copied by tcgen05.cp, 6 or 12 tiles a stage beside 768
-// clocks of products: 133 / 171.
+// clocks of products, before the other steps: 133 / 171 against 107 / 110.
 template <int FMT>
 struct Wide {
     static constexpr int KT = 256 / (4 * fp4_block(FMT));

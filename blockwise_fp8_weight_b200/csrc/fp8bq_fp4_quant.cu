@@ -9,7 +9,7 @@
 //
 // NVFP4, 16 values a block, t a positive fp32 scale of the whole tensor:
 //     s = e4m3(min((a / 6) / t, 448))           IEEE fp32 divisions
-//     d = s * t,  r = 1 / d (0 if d = 0)        each rounded to fp32
+//     d = s * t,  r = 1 / d (0 if d = 0)        each rounded to fp32, r finite
 //     code = e2m1(x * r)                        the product rounded to fp32
 //
 // A block that holds an infinity or a NaN gets the NaN scale and zero codes.

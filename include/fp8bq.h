@@ -246,7 +246,8 @@ FP8BQ_API fp8bq_status fp8bq_tensor_scale(const fp8bq_scale_desc *desc_table, in
  *       value = e2m1 value * 2^S
  *   FP8BQ_NVFP4  16 values a scale (e4m3), and one fp32 scale t of the tensor:
  *       s     = e4m3(min((a / 6) / t, 448))     (IEEE fp32 divisions)
- *       d     = s * t;  r = 1 / d, 0 if d = 0   (each rounded to fp32)
+ *       d     = s * t;  r = 1 / d, 0 if d = 0   (each rounded to fp32; the largest
+ *               finite value where 1 / d is beyond it)
  *       code  = e2m1(x * r)                     (the product rounded to fp32)
  *       value = e2m1 value * s * t
  *       t > 0; NULL means 1.  max|X| / (6 * 448) makes the largest block's s
@@ -325,8 +326,9 @@ typedef struct fp8bq_fp4_operand {
  *
  * a is [M, K] (tokens), b and up are [N, K] (weights, one row for each output
  * column), out is [M, N] in bf16 or fp32.  Products and sums are those of the
- * tensor cores, held in fp32; tensor scales, the activation and the gate's
- * product are fp32; the result is rounded once.  A K range may be summed in
+ * tensor cores, held in fp32.  A sum is multiplied by the fp32 product of its two
+ * tensor scales, which must be finite; that, the activation and the gate's
+ * product are fp32, and the result is rounded once.  A K range may be summed in
  * parts, always the same ones in the same order for the same call: results
  * repeat bit for bit.
  *
