@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
     __shared__ volatile int abort_flag;
     uint8_t *ring = raw + ((1024u - (dev::smem_addr(raw) & 1023u)) & 1023u);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same for a warp
     const uint32_t split = (uint32_t)p.split, rank = split > 1 ? dev::cluster_rank() : 0;
     int k0 = 0, k1 = p.stages_k;  // this CTA's stages (fewer than 2^23)
     if (split > 1) {
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
         }
     };
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && dev::elect_one()) {
         bool dropped = false, ok = true;
         int i = 0;  // stages loaded
         Slot<S::kStages> s;
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
             if (!dev::mbar_wait_bounded(&full[st], (fills - 1) & 1, kDrainNs, nullptr))
                 atomicOr(&g_fp4_error_word, 2u);
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && dev::elect_one()) {
         constexpr uint32_t word = dev::mma_word(FMT, 128, NT);
         bool ok = true;
         int n = 0;  // tiles
@@ -661,7 +662,8 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
     __shared__ volatile int abort_flag;
     uint8_t *ring = raw + ((1024u - (dev::smem_addr(raw) & 1023u)) & 1023u);
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same for a warp
     const uint32_t rank = dev::cluster_rank();
     constexpr int kWidth = GATED ? 128 : 256;
     if (tid == 0) {
@@ -699,7 +701,7 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
     };
 
     WideWalk w(p, kWidth);
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && dev::elect_one()) {
         auto at = [&](int map) { return (p.moves >> map) & 1u ? w.e : 0; };
         bool dropped = false, ok = true;
         int i = 0;  // stages loaded
@@ -745,7 +747,7 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
                 !dev::mbar_wait_bounded(&landed[st], (fills - 1) & 1, kDrainNs, nullptr))
                 atomicOr(&g_fp4_error_word, 2u);
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0 && dev::elect_one()) {
         constexpr uint32_t word = dev::mma_word(FMT, 256, 256);
         bool ok = true;
         int n = 0;  // tiles
