@@ -580,7 +580,7 @@ struct Wide {
     static constexpr int kScales = 416;
     static constexpr int kSfCols = 12 * KT;                    // a stage's: tokens, then weight
     static constexpr int kSfBufs = (512 - kScales) / kSfCols;
-    static constexpr int kThreads = 512;
+    static constexpr int kThreads = 640;
     static_assert(kSfBufs >= 2 && kSfBufs <= kStages, "scale buffers");
 };
 
@@ -651,7 +651,7 @@ struct WideWalk {
 };
 
 template <int FMT, bool GATED, bool BF16>
-__global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4MmParams p) {
+__global__ void __launch_bounds__(640, 1) k_fp4_wide(const __grid_constant__ Fp4MmParams p) {
     using S = Wide<FMT>;
     extern __shared__ uint8_t raw[];
     // full (codes), scaled, drained: the first CTA's count for both; landed
@@ -792,13 +792,18 @@ __global__ void __launch_bounds__(512, 1) k_fp4_wide(const __grid_constant__ Fp4
         }
         dev::mma_commit_pair_here(&done);
         if (!dev::mbar_wait_bounded(&done, 0, kDrainNs, nullptr)) atomicOr(&g_fp4_error_word, 2u);
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= 4 && (warp < 8 || warp >= 16)) {
+        const int turn = warp >> 4;
         const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
         bool ok = true;
         Slot<S::kStages> s, old;  // `old`: kSfBufs stages behind
         Slot<S::kSfBufs> f;
         for (int i = 0; ok && w.next();) {
             for (int k = 0; k < p.stages_k; ++k, ++i, s.next(), f.next()) {
+                if ((i & 1) != turn) {
+                    if (i >= S::kSfBufs) old.next();
+                    continue;
+                }
                 bool here = dev::mbar_wait_bounded(&landed[s.at], s.parity, p.wait_limit_ns,
                                                    &abort_flag);
                 if (rank == 0)
