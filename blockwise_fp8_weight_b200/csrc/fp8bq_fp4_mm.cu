@@ -581,10 +581,13 @@ struct Wide {
     static constexpr int kSfCols = 12 * KT;                    // a stage's: tokens, then weight
     static constexpr int kSfBufs = (512 - kScales) / kSfCols;
     static constexpr int kThreads = 640;
+    static constexpr int kStore = 1024;                        // a storing warp's, of eight
     static_assert(kSfBufs >= 2 && kSfBufs <= kStages, "scale buffers");
+    static_assert(1024 + kStages * kStage + 8 * kStore <= kSmem, "room to store");
 };
 
-// 16 consecutive outputs of a row, from column n.
+// 16 consecutive outputs of a row, from column n; rows begin at multiples of 16
+// bytes (fp32: 32).
 template <bool BF16>
 __device__ __forceinline__ void store16(const Fp4MmParams &p, int64_t e, int64_t m, int n,
                                         const float (&v)[16]) {
@@ -597,9 +600,9 @@ __device__ __forceinline__ void store16(const Fp4MmParams &p, int64_t e, int64_t
         for (int j = 0; j < 8; ++j)
             w[j] = BF16 ? bf16x2(v[(c + 2 * j) & 15], v[(c + 2 * j + 1) & 15])
                         : __float_as_uint(v[(c + j) & 15]);
-        if (n + c + PER <= p.N && p.store_align >= 16) {
+        if (n + c + PER <= p.N) {
             if (!FP8BQ_IN(MM_SPAN(p.out, p.out_bytes), dst, 32)) continue;
-            if (p.store_align >= 32) {
+            if (!BF16 || p.store_align >= 32) {
                 asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
                              "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
                              "r"(w[6]), "r"(w[7])
@@ -619,6 +622,59 @@ __device__ __forceinline__ void store16(const Fp4MmParams &p, int64_t e, int64_t
                         *(uint32_t *)(dst + j * 4) = w[j & 7];
                 }
         }
+    }
+}
+
+// The same of a warp's 32 rows from row m, `rows` of them to be stored, where
+// rows begin at multiples of W bytes only: 32 bytes a row at a time through
+// shared memory, so that a store covers 32 bytes of W rows rather than W of 32.
+// Measured on B200, 8192 tokens, K = 512, and with every lane storing its own
+// row: 6148 fp32 outputs (W = 16) 81 us, 127; 6143 (W = 4) 112, 350; 6148 bf16
+// outputs (4) 47, 470; 6143 (2) 62, 470.  (6152 bf16 outputs, 16: 37, 40, but
+// gated 70, 62; 6144 fp32 outputs, 32: 64, 51.  Those the lanes store.)
+template <bool BF16, int W>
+__device__ __forceinline__ void store_pieces(const Fp4MmParams &p, int64_t e, int64_t m, int rows,
+                                             int n, const char *buf, int lane) {
+    constexpr int ES = BF16 ? 2 : 4;
+    const int r = lane / (32 / W), c = lane % (32 / W) * W / ES;
+    char *dst = (char *)p.out + (e * p.obs + (m + r) * p.ldo + n + c) * ES;
+    buf += lane * W;
+#pragma unroll
+    for (int j = 0; j < 32; j += W, buf += 32 * W, dst += (int64_t)W * p.ldo * ES) {
+        if (j + r >= rows) break;
+        if (n + c + W / ES <= p.N) {
+            if (!FP8BQ_IN(MM_SPAN(p.out, p.out_bytes), dst, W)) continue;
+            if constexpr (W == 16) *(uint4 *)dst = *(const uint4 *)buf;
+            else if constexpr (W == 4) *(uint32_t *)dst = *(const uint32_t *)buf;
+            else *(uint16_t *)dst = *(const uint16_t *)buf;
+        } else {
+#pragma unroll
+            for (int q = 0; q < W / ES; ++q)
+                if (n + c + q < p.N && FP8BQ_IN(MM_SPAN(p.out, p.out_bytes), dst + q * ES, ES)) {
+                    if constexpr (BF16)
+                        *(uint16_t *)(dst + 2 * q) = *(const uint16_t *)(buf + 2 * q);
+                    else
+                        *(uint32_t *)(dst + 4 * q) = *(const uint32_t *)(buf + 4 * q);
+                }
+        }
+    }
+}
+template <bool BF16, int W>
+__device__ __forceinline__ void store16_staged(const Fp4MmParams &p, int64_t e, int64_t m, int rows,
+                                               int n, const float (&v)[16], char *buf, int lane) {
+    constexpr int PER = BF16 ? 16 : 8;                         // outputs in 32 bytes
+#pragma unroll
+    for (int c = 0; c < 16; c += PER) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            w[j] = BF16 ? bf16x2(v[(c + 2 * j) & 15], v[(c + 2 * j + 1) & 15])
+                        : __float_as_uint(v[(c + j) & 15]);
+        __syncwarp();  // the last piece is read
+        *(uint4 *)(buf + lane * 32) = make_uint4(w[0], w[1], w[2], w[3]);
+        *(uint4 *)(buf + lane * 32 + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+        __syncwarp();
+        store_pieces<BF16, W>(p, e, m, rows, n + c, buf, lane);
     }
 }
 
@@ -650,7 +706,8 @@ struct WideWalk {
     }
 };
 
-template <int FMT, bool GATED, bool BF16>
+// ALIGN: rows of the output begin at multiples of so many bytes, or of more.
+template <int FMT, bool GATED, bool BF16, int ALIGN>
 __global__ void __launch_bounds__(640, 1) k_fp4_wide(const __grid_constant__ Fp4MmParams p) {
     using S = Wide<FMT>;
     extern __shared__ uint8_t raw[];
@@ -836,6 +893,7 @@ __global__ void __launch_bounds__(640, 1) k_fp4_wide(const __grid_constant__ Fp4
         }
     } else if (warp >= 8) {
         const int quarter = warp & 3, half = (warp - 8) >> 2;
+        [[maybe_unused]] char *buf = (char *)ring + S::kStages * S::kStage + (warp - 8) * S::kStore;
         const uint32_t drained_bar = dev::peer_addr(dev::smem_addr(&drained), 0);
         for (int n = 0; w.next(); ++n) {
             const bool here =
@@ -846,8 +904,8 @@ __global__ void __launch_bounds__(640, 1) k_fp4_wide(const __grid_constant__ Fp4
             }
             dev::tc_fence_after();
             const uint32_t d = tmem + (n & 1) * S::kOther + ((uint32_t)(quarter * 32) << 16);
-            const int64_t m = w.m0 + (int)rank * 128 + quarter * 32 + lane;
-            const bool in = m < w.valid;
+            const int m0 = w.m0 + (int)rank * 128 + quarter * 32;  // the warp's first row
+            [[maybe_unused]] const bool in = m0 + lane < w.valid;
             const float xt = MM_XT(p, w.e), alpha = __fmul_rn(xt, MM_WT(p, 0, w.e));
             const float alpha1 = GATED ? __fmul_rn(xt, MM_WT(p, 1, w.e)) : 0.0f;
             // Runs of 16 columns, every other one of them this warp's, from
@@ -879,7 +937,11 @@ __global__ void __launch_bounds__(640, 1) k_fp4_wide(const __grid_constant__ Fp4
                     }
                 }
                 const int c = w.n0 + 16 * run(i);
-                if (in && c < p.N) store16<BF16>(p, w.e, m, c, v);
+                if constexpr (ALIGN < (BF16 ? 16 : 32)) {
+                    if (c < p.N) store16_staged<BF16, ALIGN>(p, w.e, m0, w.valid - m0, c, v, buf, lane);
+                } else if (in && c < p.N) {
+                    store16<BF16>(p, w.e, m0 + lane, c, v);
+                }
             };
 #pragma unroll
             for (int i = 0; i < 3; ++i) {
@@ -1016,10 +1078,10 @@ cudaError_t narrow_format(const Fp4MmParams &p, bool gated, bool bf16, int token
                 : narrow_tokens<FMT, false, false>(p, tokens, st);
 }
 
-template <int FMT, bool GATED, bool BF16>
+template <int FMT, bool GATED, bool BF16, int ALIGN>
 cudaError_t wide(const Fp4MmParams &p, cudaStream_t st) {
     using S = Wide<FMT>;
-    auto kern = k_fp4_wide<FMT, GATED, BF16>;
+    auto kern = k_fp4_wide<FMT, GATED, BF16, ALIGN>;
     static PerDevice<cudaError_t> setup;
     const cudaError_t e = setup.get([&] { return set_smem(kern, S::kSmem); });
     if (e != cudaSuccess) return e;
@@ -1030,10 +1092,18 @@ cudaError_t wide(const Fp4MmParams &p, cudaStream_t st) {
                            S::kSmem, st, p);
 }
 
+template <int FMT, bool GATED, bool BF16>
+cudaError_t wide_store(const Fp4MmParams &p, cudaStream_t st) {
+    if (!BF16 && p.store_align >= 32) return wide<FMT, GATED, BF16, BF16 ? 16 : 32>(p, st);
+    if (p.store_align >= 16) return wide<FMT, GATED, BF16, 16>(p, st);
+    if (!BF16 || p.store_align >= 4) return wide<FMT, GATED, BF16, 4>(p, st);
+    return wide<FMT, GATED, BF16, BF16 ? 2 : 4>(p, st);
+}
+
 template <int FMT>
 cudaError_t wide_format(const Fp4MmParams &p, bool gated, bool bf16, cudaStream_t st) {
-    if (gated) return bf16 ? wide<FMT, true, true>(p, st) : wide<FMT, true, false>(p, st);
-    return bf16 ? wide<FMT, false, true>(p, st) : wide<FMT, false, false>(p, st);
+    if (gated) return bf16 ? wide_store<FMT, true, true>(p, st) : wide_store<FMT, true, false>(p, st);
+    return bf16 ? wide_store<FMT, false, true>(p, st) : wide_store<FMT, false, false>(p, st);
 }
 
 }  // namespace
