@@ -107,8 +107,12 @@ struct Fp4MmParams {
 // tokens: the tile's width in tokens (16, 32, 64, 128 or 256; gated at most 128)
 cudaError_t launch_fp4_mm_narrow(const Fp4MmParams &p, int format, bool gated, bool out_bf16,
                                  int tokens, cudaStream_t st);
-// Which kernel: 0 the one for many tokens, else the tile's width in tokens.
-int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated, double *us);
+// Whether the many-token kernel's outputs pass through shared memory.
+constexpr bool fp4_staged(int store_align, int esize) { return store_align < 8 * esize; }
+// Which kernel: 0 the one for many tokens, else the tile's width in tokens; `us`:
+// the microseconds it takes about.
+int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated, bool staged,
+               double *us);
 // Tiles of 256 tokens by 256 outputs (gated: 128) on pairs of SMs.
 cudaError_t launch_fp4_mm_wide(const Fp4MmParams &p, int format, bool gated, bool out_bf16,
                                cudaStream_t st);

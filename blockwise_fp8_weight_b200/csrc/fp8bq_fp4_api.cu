@@ -326,8 +326,12 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     if (sd != FP8BQ_OK) return sd;
 
     const int64_t kb = fp4_row_bytes(D.K), stages = (kb + 127) / 128;
+    int store_align = es;
+    for (int a : {4, 8, 16, 32})
+        if ((uintptr_t)D.out % a == 0 && D.ld_out * es % a == 0 && obs * es % a == 0)
+            store_align = a;
     double us = 0;
-    const int tokens = fp4_choose(D.M, D.N, stages, D.batch, gated, &us);
+    const int tokens = fp4_choose(D.M, D.N, stages, D.batch, gated, fp4_staged(store_align, es), &us);
     const bool wide = tokens == 0;
     Fp4MmParams p;
     std::memset(&p, 0, sizeof p);
@@ -352,10 +356,7 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     p.stages_k = (int32_t)stages;
     p.mma_k = (int32_t)((kb + 31) / 32);
     p.split = 1;
-    p.store_align = es;
-    for (int a : {4, 8, 16, 32})
-        if ((uintptr_t)D.out % a == 0 && D.ld_out * es % a == 0 && obs * es % a == 0)
-            p.store_align = a;
+    p.store_align = store_align;
     for (int i = 0; i < n; ++i)  // a stack stride of 0: one matrix for the whole stack
         p.moves |= (mats[i].cbs ? 1u : 0u) << (2 * i) | (mats[i].sbs ? 2u : 0u) << (2 * i);
     p.overlap = fp4_overlap(stream, us);

@@ -937,7 +937,7 @@ __global__ void __launch_bounds__(640, 1) k_fp4_wide(const __grid_constant__ Fp4
                     }
                 }
                 const int c = w.n0 + 16 * run(i);
-                if constexpr (ALIGN < (BF16 ? 16 : 32)) {
+                if constexpr (fp4_staged(ALIGN, BF16 ? 2 : 4)) {
                     if (c < p.N) store16_staged<BF16, ALIGN>(p, w.e, m0, w.valid - m0, c, v, buf, lane);
                 } else if (in && c < p.N) {
                     store16<BF16>(p, w.e, m0 + lane, c, v);
@@ -1121,29 +1121,33 @@ cudaError_t launch_fp4_mm_wide(const Fp4MmParams &p, int format, bool gated, boo
 //     begin + stage * (stages of a CTA)
 //           + max(again * (stages), round) * (rounds - 1)
 // microseconds, rounds = tiles over the tiles that run at once; `round` is the
-// time to store a tile.  Fitted to B200, 1000 x 4100 to 12288 x 4096 and 4096 x
-// 12288, stacks of 8 to 128 of 768 x 2048 to 4096 x 4096, 1 to 2048 tokens, mxfp4
-// (measured, us, many-token / 64 / 128 / 256 wide tiles):
-//     515 tokens, 1000 x 4100    13.7 / 10.7 /  9.8 / 11.5
-//     256 tokens, 4096 x 4096    12.2 / 10.7 / 10.2 / 10.9
-//     256 tokens, 12288 x 4096   13.0 / 20.2 / 20.3 / 17.1
-//     300 tokens, 4096 x 12288   26.3 / 26.5 / 25.7 / 18.5
-//     1024 tokens, 6144 x 4096   20.5 / 29.1 / 27.6 / 30.3
-//     gated, 256 x 4096 x 4096   12.8 / 15.0 / 13.4
-//     gated, 64 x 12288 x 4096   21.3 / 15.8 / 15.9
-//     128 of 128 x 2048 x 768    41.4 / 46.0 / 61.4 / 71.2
-//     128 of 64 x 2048 x 768     32.1 / 26.3 / 36.9 / 46.5
-int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated, double *us) {
+// time to store a tile, and `staged` what a round of the many-token kernel
+// takes longer where its outputs pass through shared memory.  Fitted to B200,
+// 1000 x 4100 to 12288 x 4096 and 4096 x 12288, stacks of 8 to 128 of 768 x 2048
+// to 4096 x 4096, 40 to 4000 tokens, mxfp4: the choice costs 1 % of the best
+// one's time on average (measured, us, many-token / 64 / 128 / 256 wide tiles):
+//     515 tokens, 1000 x 4100    13.0 / 10.2 /  9.3 / 11.3
+//     1500 tokens, 1001 x 700     8.7 /  5.5 /  5.6 /  9.3
+//     256 tokens, 4096 x 4096     9.9 /  9.6 /  8.7 / 10.5
+//     256 tokens, 12288 x 4096   10.5 / 16.2 / 15.3 / 15.5
+//     300 tokens, 4096 x 12288   19.3 / 20.7 / 19.0 / 16.7
+//     1024 tokens, 6144 x 4096   16.3 / 22.7 / 20.8 / 27.6
+//     gated, 256 x 4096 x 4096   10.6 / 10.8 / 11.7
+//     gated, 64 x 12288 x 4096   15.9 / 10.9 / 11.5
+//     128 of 128 x 2048 x 768    41.0 / 44.8 / 60.3 / 66.8
+//     128 of 64 x 2048 x 768     29.6 / 26.1 / 36.2 / 42.5
+int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated, bool staged,
+               double *us) {
     struct Cost {
         int tokens;
-        double begin, stage, again, round;
+        double begin, stage, again, round, staged;
     };
-    static constexpr Cost plain[] = {{16, 4.9, 0.33, 0.40, 2.5}, {32, 5.3, 0.33, 0.42, 2.5},
-                                     {0, 4.8, 0.45, 0.50, 2.6},  {64, 6.2, 0.40, 0.45, 2.8},
-                                     {128, 7.0, 0.36, 0.55, 3.9}, {256, 8.6, 0.50, 0.90, 4.5}};
-    static constexpr Cost both[] = {{16, 5.5, 0.45, 0.60, 2.6}, {32, 6.5, 0.45, 0.60, 2.6},
-                                    {0, 4.8, 0.47, 0.55, 2.8},  {64, 8.3, 0.42, 0.57, 2.8},
-                                    {128, 9.5, 0.55, 1.00, 5.8}};
+    static constexpr Cost plain[] = {{16, 4.5, 0.33, 0.40, 2.5, 0},  {32, 4.9, 0.33, 0.42, 2.5, 0},
+                                     {0, 5.7, 0.27, 0.44, 2.2, 1.9}, {64, 6.7, 0.33, 0.43, 3.1, 0},
+                                     {128, 6.4, 0.26, 0.36, 3.2, 0}, {256, 8.0, 0.32, 0.70, 3.4, 0}};
+    static constexpr Cost both[] = {{16, 5.1, 0.45, 0.60, 2.6, 0},  {32, 6.1, 0.45, 0.60, 2.6, 0},
+                                    {0, 5.8, 0.30, 0.42, 2.9, 1.7}, {64, 6.7, 0.31, 0.44, 3.1, 0},
+                                    {128, 8.6, 0.37, 0.90, 4.4, 0}};
     const double sms = sm_count();
     const int first = M <= 16 ? 0 : M <= 32 ? 1 : 2, last = M <= 32 ? first : gated ? 4 : 5;
     int best = 0;
@@ -1160,7 +1164,8 @@ int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated, 
                     share = (double)((stages + s - 1) / s);
         const double rounds = (double)(int64_t)((tiles + once - 1) / once);
         const double again = c.again * stages > c.round ? c.again * stages : c.round;
-        const double t = c.begin + c.stage * share + again * (rounds - 1);
+        const double t = c.begin + c.stage * share + again * (rounds - 1) +
+                         (staged ? c.staged * rounds : 0);
         if (i == first || t < *us) {
             *us = t;
             best = c.tokens;
