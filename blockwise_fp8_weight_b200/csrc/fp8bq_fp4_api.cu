@@ -12,7 +12,7 @@ using namespace fp8bq;
 
 bool fp8bq::fp4_overlap(cudaStream_t st, double us) {
     if (!pdl_enabled()) return false;
-    if (us > 8.5) return true;
+    if (us > 6.5) return true;
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) {
         cudaGetLastError();

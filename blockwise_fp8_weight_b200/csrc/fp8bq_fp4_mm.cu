@@ -495,9 +495,11 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
                     v[j] = __uint_as_float(g[j]) * alpha;
                     if constexpr (GATED) v[j] = silu(v[j]) * (__uint_as_float(u[j]) * alpha1);
                 }
-                if (BF16 && p.store_align >= 4) {
+                if (NT == 16 && BF16 && p.store_align >= 4) {
                     // two tokens at a time: an even lane stores its and its
                     // neighbour's output of the first, an odd one of the second
+                    // (16 tokens against 151936 x 512 on B200: 7.2 us, by element
+                    // 7.8; wider tiles are 5 to 30 % slower this way)
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
                         const bool odd = lane & 1;
@@ -1124,30 +1126,30 @@ cudaError_t launch_fp4_mm_wide(const Fp4MmParams &p, int format, bool gated, boo
 // time to store a tile, and `staged` what a round of the many-token kernel
 // takes longer where its outputs pass through shared memory.  Fitted to B200,
 // 1000 x 4100 to 12288 x 4096 and 4096 x 12288, stacks of 8 to 128 of 768 x 2048
-// to 4096 x 4096, 40 to 4000 tokens, mxfp4: the choice costs 1 % of the best
+// to 4096 x 4096, 40 to 8192 tokens, mxfp4: the choice costs 1 to 2 % of the best
 // one's time on average (measured, us, many-token / 64 / 128 / 256 wide tiles):
 //     515 tokens, 1000 x 4100    13.0 / 10.2 /  9.3 / 11.3
-//     1500 tokens, 1001 x 700     8.7 /  5.5 /  5.6 /  9.3
+//     1500 tokens, 1001 x 700     8.7 /  5.5 /  5.6 /  9.2
+//     8192 tokens, 6148 x 512    46.1 / 52.5 / 61.3 / 61.5
 //     256 tokens, 4096 x 4096     9.9 /  9.6 /  8.7 / 10.5
 //     256 tokens, 12288 x 4096   10.5 / 16.2 / 15.3 / 15.5
 //     300 tokens, 4096 x 12288   19.3 / 20.7 / 19.0 / 16.7
-//     1024 tokens, 6144 x 4096   16.3 / 22.7 / 20.8 / 27.6
+//     1024 tokens, 6144 x 4096   16.5 / 22.5 / 19.8 / 23.0
 //     gated, 256 x 4096 x 4096   10.6 / 10.8 / 11.7
 //     gated, 64 x 12288 x 4096   15.9 / 10.9 / 11.5
-//     128 of 128 x 2048 x 768    41.0 / 44.8 / 60.3 / 66.8
-//     128 of 64 x 2048 x 768     29.6 / 26.1 / 36.2 / 42.5
+//     128 of 128 x 2048 x 768    41.0 / 39.0 / 41.0 / 51.1
 int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated, bool staged,
                double *us) {
     struct Cost {
         int tokens;
         double begin, stage, again, round, staged;
     };
-    static constexpr Cost plain[] = {{16, 4.5, 0.33, 0.40, 2.5, 0},  {32, 4.9, 0.33, 0.42, 2.5, 0},
-                                     {0, 5.7, 0.27, 0.44, 2.2, 1.9}, {64, 6.7, 0.33, 0.43, 3.1, 0},
-                                     {128, 6.4, 0.26, 0.36, 3.2, 0}, {256, 8.0, 0.32, 0.70, 3.4, 0}};
+    static constexpr Cost plain[] = {{16, 4.5, 0.33, 0.40, 2.5, 0},  {32, 4.9, 0.33, 0.42, 2.1, 0},
+                                     {0, 5.7, 0.28, 0.43, 2.1, 2.0}, {64, 6.3, 0.34, 0.43, 2.1, 0},
+                                     {128, 6.2, 0.24, 0.36, 2.4, 0}, {256, 8.2, 0.28, 0.61, 5.2, 0}};
     static constexpr Cost both[] = {{16, 5.1, 0.45, 0.60, 2.6, 0},  {32, 6.1, 0.45, 0.60, 2.6, 0},
-                                    {0, 5.8, 0.30, 0.42, 2.9, 1.7}, {64, 6.7, 0.31, 0.44, 3.1, 0},
-                                    {128, 8.6, 0.37, 0.90, 4.4, 0}};
+                                    {0, 5.9, 0.30, 0.43, 2.7, 1.5}, {64, 6.5, 0.30, 0.43, 2.35, 0},
+                                    {128, 8.6, 0.34, 0.73, 4.2, 0}};
     const double sms = sm_count();
     const int first = M <= 16 ? 0 : M <= 32 ? 1 : 2, last = M <= 32 ? first : gated ? 4 : 5;
     int best = 0;
