@@ -560,14 +560,17 @@ __global__ void __launch_bounds__(384, Narrow<FMT, GATED, NT>::kTwo ? 2 : 1)
 // two sums of an output lie 128 columns apart in the same tensor-memory lane.
 //
 // Persistent: a pair walks over tiles.  In each CTA warp 0 loads (one lane),
-// warps 4-7 bring the scales into tensor memory, warps 8-15 store; warp 1 of
+// warps 4-7 and 16-19 bring the scales of every other stage into tensor memory
+// (one group of four needs about 700 clocks a stage beside 512 of products, by
+// the latency of its waits and instructions: 91 us instead of 83, nvfp4 102
+// instead of 90), warps 8-15 store; warp 1 of
 // the first CTA issues the products of both.  The sums of successive tiles
 // alternate between columns [0, 256) and [160, 416), so the next tile is
 // multiplied while this one is stored; the 96 columns that both use are read
 // first, and the next tile waits for those alone.  The scales' buffers take
 // the last 96 columns.
 //
-// Measured on B200, 8192 tokens against 6144 x 4096 (mxfp4 / nvfp4): 92 / 103 us;
+// Measured on B200, 8192 tokens against 6144 x 4096 (mxfp4 / nvfp4): 82 / 88 us;
 // with the scales copied by tcgen05.cp, 6 or 12 tiles a stage beside 768
 // clocks of products, before the other steps: 133 / 171 against 107 / 110.
 template <int FMT>
