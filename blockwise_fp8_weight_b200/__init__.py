@@ -779,7 +779,8 @@ def quant_weights_fp4(weights: Iterable, format="mxfp4", stream=None):
     with _on_stream(stream):
         if format == "nvfp4":
             ts = tensor_scales([w if w.is_contiguous() else w.contiguous() for _, w in named],
-                               stream=stream) / 6.0
+                               stream=stream)
+            ts = ts / ts.new_full((), 6.0)  # by a Python number: times its rounded reciprocal
         made = [(torch.empty(cs, dtype=torch.uint8, device=w.device),
                  torch.empty(ss, dtype=torch.uint8, device=w.device))
                 for (cs, ss, _), (_, w) in zip(recs, named)]
