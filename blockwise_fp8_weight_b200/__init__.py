@@ -211,6 +211,8 @@ def lib() -> ctypes.CDLL:
             L.fp8bq_fp4_dequantize.argtypes = [vp, vp, i64, i64, i64, i32, vp, i64, vp, i32, i64,
                                                i64, vp]
             L.fp8bq_fp4_dequantize.restype = i32
+            L.fp8bq_fp4_tensor_scale.argtypes = [ctypes.POINTER(fp8bq_scale_desc), i32, vp, vp]
+            L.fp8bq_fp4_tensor_scale.restype = i32
             # the descriptor: a fp8bq_fp4_matmul_desc by reference, or its bytes
             L.fp8bq_fp4_matmul.argtypes = [vp, vp]
             L.fp8bq_fp4_matmul.restype = i32
@@ -297,6 +299,14 @@ def fp8bq_fp4_quantize_batched(desc_table, n_tensors=None, stream=None) -> int:
         desc_table = (fp8bq_fp4_desc * len(desc_table))(*desc_table)
     n = len(desc_table) if n_tensors is None else n_tensors
     return lib().fp8bq_fp4_quantize_batched(desc_table, n, _stream(stream))
+
+
+def fp8bq_fp4_tensor_scale(desc_table, scale_out, n_tensors=None, stream=None) -> int:
+    """``fp8bq_fp4_tensor_scale`` of the C ABI.  Returns the status code."""
+    if not isinstance(desc_table, ctypes.Array):
+        desc_table = (fp8bq_scale_desc * len(desc_table))(*desc_table)
+    n = len(desc_table) if n_tensors is None else n_tensors
+    return lib().fp8bq_fp4_tensor_scale(desc_table, n, _ptr(scale_out), _stream(stream))
 
 
 def fp8bq_fp4_dequantize(codes, scales, batch: int, M: int, K: int, format: int, tensor_scale,
@@ -506,6 +516,10 @@ def tensor_scales(tensors, stream=None):
     """Per-tensor FP8 scales max(max|x|, eps) / 448 of contiguous bf16/fp32
     CUDA tensors (e.g. this step's Q, K and V), in one grouped call; returns a
     float32 CUDA tensor of len(tensors) scales."""
+    return _tensor_scales(fp8bq_tensor_scale, "tensor_scales", tensors, stream)
+
+
+def _tensor_scales(call, what: str, tensors, stream):
     import torch
     tensors = list(tensors)
     if not tensors:
@@ -521,7 +535,7 @@ def tensor_scales(tensors, stream=None):
         d = fp8bq_scale_desc()
         d.x, d.numel, d.dtype_in, d.reserved = _ptr(t), t.numel(), _dtype_code(t), 0
         descs.append(d)
-    check(fp8bq_tensor_scale(descs, out, stream=stream), "tensor_scales")
+    check(call(descs, out, stream=stream), what)
     return out
 
 
@@ -764,8 +778,9 @@ def quant_weights_fp4(weights: Iterable, format="mxfp4", stream=None):
     """Quantize every (name, tensor) pair to 4 bits in one grouped call and
     return the list a rollout engine loads: (name, codes), (name + "_scale",
     scales) and, for ``"nvfp4"``, (name + "_scale_2", tensor scale) for each
-    input, in input order.  The tensor scale is max(max|w|, eps) / (448 * 6),
-    so that the largest block's scale is 448."""
+    input, in input order.  The tensor scale is max(max|w|, eps) / 448 / 6 over
+    the finite values, so that the largest finite block's scale is 448; a block
+    with an infinity or a NaN, and no other, becomes NaN."""
     _, block = _fp4_format(format)
     named = list(weights)
     if not named:
@@ -778,9 +793,9 @@ def quant_weights_fp4(weights: Iterable, format="mxfp4", stream=None):
     ts = None
     with _on_stream(stream):
         if format == "nvfp4":
-            ts = tensor_scales([w if w.is_contiguous() else w.contiguous() for _, w in named],
-                               stream=stream)
-            ts = ts / ts.new_full((), 6.0)  # by a Python number: times its rounded reciprocal
+            ts = _tensor_scales(fp8bq_fp4_tensor_scale, "quant_weights_fp4",
+                                [w if w.is_contiguous() else w.contiguous() for _, w in named],
+                                stream)
         made = [(torch.empty(cs, dtype=torch.uint8, device=w.device),
                  torch.empty(ss, dtype=torch.uint8, device=w.device))
                 for (cs, ss, _), (_, w) in zip(recs, named)]

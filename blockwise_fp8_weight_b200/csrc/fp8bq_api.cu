@@ -838,7 +838,7 @@ fp8bq_status run_dequant(const fp8bq_dequant_desc *t, int n, cudaStream_t stream
 
 template <int MAXD>
 cudaError_t launch_scale_group(const fp8bq_scale_desc *t, const std::vector<int> &idx, int es,
-                               float *scale_out, uint64_t out_bytes, cudaStream_t st) {
+                               float *scale_out, uint64_t out_bytes, bool nvfp4, cudaStream_t st) {
     static thread_local ScalePack<MAXD> p;
     size_t i = 0;
     while (i < idx.size()) {
@@ -861,13 +861,14 @@ cudaError_t launch_scale_group(const fp8bq_scale_desc *t, const std::vector<int>
             ++i;
         }
         if (p.total == 0) continue;
-        const cudaError_t e = launch_scale_amax<MAXD>(p, es, st);
+        const cudaError_t e = launch_scale_amax<MAXD>(p, es, nvfp4, st);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
-fp8bq_status run_tensor_scale(const fp8bq_scale_desc *t, int n, float *scale_out,
+// nvfp4: over finite values alone, and divided by 6.
+fp8bq_status run_tensor_scale(const fp8bq_scale_desc *t, int n, float *scale_out, bool nvfp4,
                               cudaStream_t stream) {
     if (n < 0) return FP8BQ_ERR_ARG;
     if (n == 0) return FP8BQ_OK;
@@ -900,11 +901,11 @@ fp8bq_status run_tensor_scale(const fp8bq_scale_desc *t, int n, float *scale_out
         const int es = g ? 4 : 2;
         const cudaError_t e =
             groups[g].size() <= (size_t)kMaxDescSmall
-                ? launch_scale_group<kMaxDescSmall>(t, groups[g], es, scale_out, out_bytes, stream)
-                : launch_scale_group<kMaxDescLarge>(t, groups[g], es, scale_out, out_bytes, stream);
+                ? launch_scale_group<kMaxDescSmall>(t, groups[g], es, scale_out, out_bytes, nvfp4, stream)
+                : launch_scale_group<kMaxDescLarge>(t, groups[g], es, scale_out, out_bytes, nvfp4, stream);
         if (e != cudaSuccess) return FP8BQ_ERR_DEVICE;
     }
-    return launch_scale_finalize(scale_out, n, out_bytes, stream) == cudaSuccess
+    return launch_scale_finalize(scale_out, n, out_bytes, nvfp4, stream) == cudaSuccess
                ? FP8BQ_OK
                : FP8BQ_ERR_DEVICE;
 }
@@ -942,7 +943,16 @@ extern "C" {
 
 fp8bq_status fp8bq_tensor_scale(const fp8bq_scale_desc *desc_table, int n_tensors,
                                 float *scale_out, cudaStream_t stream) {
-    return run_tensor_scale(desc_table, n_tensors, scale_out, stream);
+    return run_tensor_scale(desc_table, n_tensors, scale_out, false, stream);
+}
+
+fp8bq_status fp8bq_fp4_tensor_scale(const fp8bq_scale_desc *desc_table, int n_tensors,
+                                    float *scale_out, cudaStream_t stream) {
+    try {  // the list of each type's tensors may find no memory
+        return run_tensor_scale(desc_table, n_tensors, scale_out, true, stream);
+    } catch (...) {
+        return FP8BQ_ERR_DEVICE;
+    }
 }
 
 fp8bq_status fp8bq_quantize(const void *x, fp8bq_dtype dtype_in, int64_t M, int64_t N, int64_t ld,

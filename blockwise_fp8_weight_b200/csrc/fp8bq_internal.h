@@ -225,10 +225,11 @@ struct ScalePack {
 };
 static_assert(sizeof(ScalePack<kMaxDescLarge>) < 32000, "kernel parameter limit");
 template <int MAXD>
-cudaError_t launch_scale_amax(const ScalePack<MAXD> &p, int esize, cudaStream_t st);
+cudaError_t launch_scale_amax(const ScalePack<MAXD> &p, int esize, bool finite, cudaStream_t st);
 // out_bytes: the extent of scale_out that the bounds checks of checked builds take
 cudaError_t launch_scale_zero(float *scale_out, int n, uint64_t out_bytes, cudaStream_t st);
-cudaError_t launch_scale_finalize(float *scale_out, int n, uint64_t out_bytes, cudaStream_t st);
+cudaError_t launch_scale_finalize(float *scale_out, int n, uint64_t out_bytes, bool by_six,
+                                  cudaStream_t st);
 
 // Device error word access (fp8bq_tma.cu).
 cudaError_t read_and_clear_error_word(uint32_t *out);

@@ -13,19 +13,46 @@
 // was zeroed first; for non-negative floats the integer order of the bits is
 // the numeric order).  Pass 2 (k_scale_finalize) turns the bits into the
 // scale in place.
+//
+// The NVFP4 tensor scales are the same over finite values alone (FINITE), and
+// divided by 6, the largest e2m1 value: a block with an infinity or a NaN has
+// the NaN scale there, and must not decide the scale of the others.
 #include "fp8bq_device.cuh"
 #include "fp8bq_internal.h"
 
 namespace fp8bq {
 namespace {
 
-template <int ESIZE>
+// Bits of a magnitude, 0 for an infinity or a NaN.
+__device__ __forceinline__ uint32_t finite_bits(uint32_t a) { return a < 0x7f800000u ? a : 0u; }
+
+template <int ESIZE, bool FINITE>
 __device__ __forceinline__ uint32_t elem_abs(const char *base, int64_t i, const dev::Span &xs) {
     if (!FP8BQ_IN(xs, base + i * ESIZE, ESIZE)) return 0;
+    uint32_t a;
     if constexpr (ESIZE == 2)
-        return ((uint32_t)__ldg((const unsigned short *)base + i) & 0x7fffu) << 16;
+        a = ((uint32_t)__ldg((const unsigned short *)base + i) & 0x7fffu) << 16;
     else
-        return __float_as_uint(__ldg((const float *)base + i)) & 0x7fffffffu;
+        a = __float_as_uint(__ldg((const float *)base + i)) & 0x7fffffffu;
+    return FINITE ? finite_bits(a) : a;
+}
+
+// Largest finite magnitude of 16 bytes, as fp32 bits.  0 * v + v makes a NaN of
+// an infinity and leaves the rest (a zero's sign aside); the maxima pass over
+// NaN; and the maximum of values that were all NaN is dropped at the end.
+__device__ __forceinline__ uint32_t finite_max_bf16(const uint4 &v) {
+    uint32_t d;
+    asm("{\n\t.reg .b32 a, b, c, e, z;\n\tmov.b32 z, 0;\n\t"
+        "fma.rn.bf16x2 a, %1, z, %1;\n\tfma.rn.bf16x2 b, %2, z, %2;\n\t"
+        "fma.rn.bf16x2 c, %3, z, %3;\n\tfma.rn.bf16x2 e, %4, z, %4;\n\t"
+        "max.xorsign.abs.bf16x2 a, a, b;\n\tmax.xorsign.abs.bf16x2 c, c, e;\n\t"
+        "max.xorsign.abs.bf16x2 %0, a, c;\n\t}"
+        : "=r"(d) : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+    return max(finite_bits((d & 0x7fffu) << 16), finite_bits(d & 0x7fff0000u));
+}
+__device__ __forceinline__ uint32_t finite_max_f32(const uint4 &v) {
+    return max(max(finite_bits(v.x & 0x7fffffffu), finite_bits(v.y & 0x7fffffffu)),
+               max(finite_bits(v.z & 0x7fffffffu), finite_bits(v.w & 0x7fffffffu)));
 }
 
 // Fold a running max into the output slot of tensor `out`: CTA-wide reduce,
@@ -44,7 +71,7 @@ __device__ __forceinline__ void flush_max(uint32_t m, uint32_t *acc, int out, ui
     __syncthreads();
 }
 
-template <int ESIZE, int MAXD>
+template <int ESIZE, bool FINITE, int MAXD>
 __global__ void __launch_bounds__(256) k_scale_amax(const __grid_constant__ ScalePack<MAXD> p) {
     dev::pdl_entry();
     constexpr int VEC = 16 / ESIZE;            // elements per 16-byte load
@@ -82,7 +109,9 @@ __global__ void __launch_bounds__(256) k_scale_amax(const __grid_constant__ Scal
             }
 #pragma unroll
             for (int j = 0; j < LOADS; ++j) {
-                if constexpr (ESIZE == 2) {
+                if constexpr (FINITE) {
+                    m = max(m, ESIZE == 2 ? finite_max_bf16(v[j]) : finite_max_f32(v[j]));
+                } else if constexpr (ESIZE == 2) {
                     const uint32_t a = dev::absmax_bf16x2(v[j].x & 0x7fff7fffu, v[j].y);
                     const uint32_t b = dev::absmax_bf16x2(v[j].z & 0x7fff7fffu, v[j].w);
                     m = max(m, dev::absmax_bits_bf16x2(dev::absmax_bf16x2(a, b)));
@@ -93,7 +122,8 @@ __global__ void __launch_bounds__(256) k_scale_amax(const __grid_constant__ Scal
                 }
             }
         } else {
-            for (int64_t i = threadIdx.x; i < len; i += 256) m = max(m, elem_abs<ESIZE>(base, i, xs));
+            for (int64_t i = threadIdx.x; i < len; i += 256)
+                m = max(m, elem_abs<ESIZE, FINITE>(base, i, xs));
         }
     }
     if (cur >= 0) flush_max(m, p.acc, p.d[cur].out, red, accs);
@@ -108,14 +138,15 @@ __global__ void k_scale_zero(float *scale_out, int n, uint64_t out_bytes) {
         if (FP8BQ_IN(os, scale_out + i, 4)) scale_out[i] = 0.0f;
 }
 
-__global__ void k_scale_finalize(float *scale_out, int n, uint64_t out_bytes) {
+__global__ void k_scale_finalize(float *scale_out, int n, uint64_t out_bytes, bool by_six) {
     dev::pdl_entry();
     [[maybe_unused]] const dev::Span os{(uint64_t)scale_out, (uint64_t)scale_out + out_bytes};
     for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) {
         if (!FP8BQ_IN(os, scale_out + i, 4)) continue;
         const uint32_t bits = reinterpret_cast<const uint32_t *>(scale_out)[i];
         const float a = fmaxf(__uint_as_float(bits), kEps);
-        scale_out[i] = __fdiv_rn(a, kFp8Max);
+        const float s = __fdiv_rn(a, kFp8Max);
+        scale_out[i] = by_six ? __fdiv_rn(s, 6.0f) : s;
     }
 }
 
@@ -132,11 +163,14 @@ __global__ void k_scale_finalize(float *scale_out, int n, uint64_t out_bytes) {
 #define FP8BQ_SCALE_CTAS_PER_SM 128
 #endif
 template <int MAXD>
-cudaError_t launch_scale_amax(const ScalePack<MAXD> &p, int esize, cudaStream_t st) {
+cudaError_t launch_scale_amax(const ScalePack<MAXD> &p, int esize, bool finite, cudaStream_t st) {
     const uint64_t cap = (uint64_t)sm_count() * FP8BQ_SCALE_CTAS_PER_SM;
     const unsigned grid = (unsigned)(p.total < cap ? (p.total ? p.total : 1) : cap);
-    return esize == 2 ? launch_kernel(k_scale_amax<2, MAXD>, grid, 256, 0, st, p)
-                      : launch_kernel(k_scale_amax<4, MAXD>, grid, 256, 0, st, p);
+    if (finite)
+        return esize == 2 ? launch_kernel(k_scale_amax<2, true, MAXD>, grid, 256, 0, st, p)
+                          : launch_kernel(k_scale_amax<4, true, MAXD>, grid, 256, 0, st, p);
+    return esize == 2 ? launch_kernel(k_scale_amax<2, false, MAXD>, grid, 256, 0, st, p)
+                      : launch_kernel(k_scale_amax<4, false, MAXD>, grid, 256, 0, st, p);
 }
 
 cudaError_t launch_scale_zero(float *scale_out, int n, uint64_t out_bytes, cudaStream_t st) {
@@ -145,15 +179,16 @@ cudaError_t launch_scale_zero(float *scale_out, int n, uint64_t out_bytes, cudaS
                          out_bytes);
 }
 
-cudaError_t launch_scale_finalize(float *scale_out, int n, uint64_t out_bytes, cudaStream_t st) {
+cudaError_t launch_scale_finalize(float *scale_out, int n, uint64_t out_bytes, bool by_six,
+                                  cudaStream_t st) {
     const int blocks = (n + 255) / 256;
     return launch_kernel(k_scale_finalize, blocks < 1 ? 1 : blocks, 256, 0, st, scale_out, n,
-                         out_bytes);
+                         out_bytes, by_six);
 }
 
-template cudaError_t launch_scale_amax<kMaxDescSmall>(const ScalePack<kMaxDescSmall> &, int,
+template cudaError_t launch_scale_amax<kMaxDescSmall>(const ScalePack<kMaxDescSmall> &, int, bool,
                                                       cudaStream_t);
-template cudaError_t launch_scale_amax<kMaxDescLarge>(const ScalePack<kMaxDescLarge> &, int,
+template cudaError_t launch_scale_amax<kMaxDescLarge>(const ScalePack<kMaxDescLarge> &, int, bool,
                                                       cudaStream_t);
 
 FP8BQ_DEFINE_BOUNDS_RECORD(bounds_record_scale)

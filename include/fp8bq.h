@@ -250,8 +250,8 @@ FP8BQ_API fp8bq_status fp8bq_tensor_scale(const fp8bq_scale_desc *desc_table, in
  *               finite value where 1 / d is beyond it)
  *       code  = e2m1(x * r)                     (the product rounded to fp32)
  *       value = e2m1 value * s * t
- *       t > 0; NULL means 1.  max|X| / (6 * 448) makes the largest block's s
- *       448: fp8bq_tensor_scale's result divided by 6.
+ *       t > 0 and finite; NULL means 1.  fp8bq_fp4_tensor_scale makes the one
+ *       with which the largest finite block's s is 448.
  *
  * e2m1() rounds to nearest, ties to even, takes magnitudes beyond 6 to 6 and
  * keeps the sign of a result that rounds to zero.  A block that holds an
@@ -293,6 +293,18 @@ FP8BQ_API fp8bq_status fp8bq_fp4_quantize(const void *x, fp8bq_dtype dtype_in, i
                                           uint8_t *scales, cudaStream_t stream);
 FP8BQ_API fp8bq_status fp8bq_fp4_quantize_batched(const fp8bq_fp4_desc *desc_table, int n_tensors,
                                                   cudaStream_t stream);
+
+/*
+ * Tensor scales for FP8BQ_NVFP4 of a list of tensors, in one grouped call:
+ *
+ *     scale_out[i] = max(max |x_i|, eps) / 448 / 6    (fp32, eps = 1e-10f)
+ *
+ * over the finite values of x_i alone, so that an infinity or a NaN costs its
+ * own block and no other.  Arguments, checks and status codes are those of
+ * fp8bq_tensor_scale.
+ */
+FP8BQ_API fp8bq_status fp8bq_fp4_tensor_scale(const fp8bq_scale_desc *desc_table, int n_tensors,
+                                              float *scale_out, cudaStream_t stream);
 
 /*
  * The values of a stack of 4-bit matrices as bf16 or fp32: matrix b at out +
