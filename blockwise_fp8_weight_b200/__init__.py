@@ -957,7 +957,10 @@ def gated_matmul_fp4(a, a_scales, gate, gate_scales, up, up_scales, format="mxfp
     """silu(a gate^T) * (a up^T), the gated half of a feed-forward block, in one
     kernel; operands and arguments as in ``matmul_fp4``.  The halves of a fused
     [(E,) 2F, K] weight may be views of it where F is a multiple of 128
-    (codes[..., :F, :], scales[..., :F // 128, :, :, :], and the rest)."""
+    (codes[..., :F, :], scales[..., :F // 128, :, :, :], and the rest).
+
+    The activation is fp32: off by at most 5 units of 2^-23 for an fp32 output,
+    and by 1.173 |v| more, far below its rounding, for a bf16 one."""
     if stream is None and rows is None and out is None:
         r = _fp4_quick("product", "gated_matmul_fp4", a, format, (1,),
                        (a, a_scales, a_tensor_scale, gate, gate_scales, gate_tensor_scale, up,

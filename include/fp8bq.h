@@ -340,9 +340,12 @@ typedef struct fp8bq_fp4_operand {
  * column), out is [M, N] in bf16 or fp32.  Products and sums are those of the
  * tensor cores, held in fp32.  A sum is multiplied by the fp32 product of its two
  * tensor scales, which must be finite; that, the activation and the gate's
- * product are fp32, and the result is rounded once.  A K range may be summed in
- * parts, always the same ones in the same order for the same call: results
- * repeat bit for bit.
+ * product are fp32, and the result is rounded once.  silu is off by at most 5
+ * units of 2^-23 of its value for fp32 outputs; for bf16 outputs, whose own
+ * rounding is 2^15 of them, by 5 + 1.173 |v| (|v| up to 87; beyond, the
+ * exponential has fp32's subnormal steps).  A K range may be summed in parts,
+ * always the same ones in the same order for the same call: results repeat bit
+ * for bit.
  *
  *   rows  device, batch int32, or NULL: only the first rows[e] rows of a[e]
  *         are used (values beyond M count as M, below 0 as 0); the rows of
