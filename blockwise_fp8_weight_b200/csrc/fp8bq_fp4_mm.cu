@@ -5,6 +5,8 @@
 // swizzle: 256 codes of a row), the scale tiles too; a scale tile is copied
 // into tensor memory next to the fp32 sums, and tcgen05.mma multiplies codes
 // and scales of 64 columns of K at a time.  Nothing is unpacked.
+#include <atomic>
+
 #include "fp8bq_fp4_device.cuh"
 
 namespace fp8bq {
@@ -12,6 +14,9 @@ namespace fp8bq {
 // Bits as in the TMA quantiser's error word: 1 a wait ran out, 2 a copy or a
 // product may still be in flight.
 __device__ uint32_t g_fp4_error_word;
+// Whether a product was launched or captured: until then the word is not read
+// (10 us a read, and the first one would load these kernels, 11 ms).
+static std::atomic<bool> g_fp4_launched{false};
 
 namespace {
 
@@ -991,6 +996,7 @@ cudaError_t set_smem(K kernel, int smem) {
 template <typename K>
 cudaError_t launch_clusters(K kern, dim3 grid, unsigned threads, unsigned cluster, int smem,
                             cudaStream_t st, const Fp4MmParams &p) {
+    g_fp4_launched.store(true, std::memory_order_relaxed);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = threads;
@@ -1192,6 +1198,8 @@ cudaError_t launch_fp4_mm_narrow(const Fp4MmParams &p, int format, bool gated, b
 }
 
 cudaError_t read_and_clear_fp4_error_word(uint32_t *out) {
+    *out = 0;
+    if (!g_fp4_launched.load(std::memory_order_relaxed)) return cudaSuccess;
     uint32_t zero = 0;
     cudaError_t e = cudaMemcpyFromSymbol(out, g_fp4_error_word, sizeof(uint32_t));
     if (e != cudaSuccess) return e;
