@@ -619,7 +619,8 @@ def quant_weights(weights: Iterable, weight_block_size=DEFAULT_BLOCK, stream=Non
 # functions do on the host is most of such a call.  The ordinary call (contiguous
 # CUDA tensors that fit each other, on the current stream) is made by the module
 # `_calls` (csrc/fp8bq_calls.c), which returns None for any other; the code here
-# then takes it, checks it and says what is wrong with it.
+# then takes it, checks it and says what is wrong with it.  It takes every call
+# where that module cannot be built.
 
 _FP4_FORMATS = {"mxfp4": (FP8BQ_MXFP4, 32), "nvfp4": (FP8BQ_NVFP4, 16)}
 # fp8bq_fp4_desc and fp8bq_fp4_matmul_desc as packed bytes
@@ -627,30 +628,43 @@ _FP4_DESC = struct.Struct("<4Q6q2i")
 _FP4_MATMUL_DESC = struct.Struct("<" + 3 * "3Q3q" + "2Q6q2i")
 
 
-_calls = None
+_calls = None  # the call module; False where it can be neither built nor loaded
 
 
 def _load_calls():
-    """The call module, built if it is missing or older than its source."""
+    """The call module, built if it is missing or older than its source; False,
+    with a warning, where that fails (no C compiler, no headers of Python)."""
     global _calls
     L = lib()
     with _lock:
         if _calls is None:
-            import importlib.machinery
-            import importlib.util
-
-            import torch
-
-            from . import build as _build
-            spec = importlib.util.spec_from_file_location(__name__ + "._calls", _build.build_calls())
-            m = importlib.util.module_from_spec(spec)
-            spec.loader.exec_module(m)
-            m.setup(torch.Tensor, torch.uint8, torch.bfloat16, torch.float32,
-                    *(ctypes.cast(f, ctypes.c_void_p).value for f in (
-                        L.fp8bq_fp4_matmul, L.fp8bq_fp4_gated_matmul, L.fp8bq_fp4_quantize_batched,
-                        L.fp8bq_fp4_dequantize)))
-            _calls = m
+            import subprocess
+            try:
+                _calls = _make_calls(L)
+            except (ImportError, OSError, RuntimeError, subprocess.SubprocessError) as e:
+                import warnings
+                warnings.warn("the 4-bit conveniences' call module cannot be built; their calls go "
+                              f"through Python, several microseconds slower: {e}", RuntimeWarning,
+                              stacklevel=2)
+                _calls = False
     return _calls
+
+
+def _make_calls(L):
+    import importlib.machinery
+    import importlib.util
+
+    import torch
+
+    from . import build as _build
+    spec = importlib.util.spec_from_file_location(__name__ + "._calls", _build.build_calls())
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.setup(torch.Tensor, torch.uint8, torch.bfloat16, torch.float32,
+            *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                L.fp8bq_fp4_matmul, L.fp8bq_fp4_gated_matmul, L.fp8bq_fp4_quantize_batched,
+                L.fp8bq_fp4_dequantize)))
+    return m
 
 
 def _fp4_quick(name: str, what: str, like, format: str, lead, args):
@@ -658,9 +672,12 @@ def _fp4_quick(name: str, what: str, like, format: str, lead, args):
     f = _FP4_FORMATS.get(format) if type(format) is str else None
     if f is None or not getattr(like, "is_cuda", False):
         return None
+    calls = _load_calls() if _calls is None else _calls
+    if not calls:
+        return None
     import torch
     dev = torch._C._cuda_getDevice()
-    r = getattr(_calls or _load_calls(), name)(
+    r = getattr(calls, name)(
         *lead, f[0], dev, torch._C._cuda_getCurrentRawStream(dev), *args)
     if type(r) is int:
         check(r, what)

@@ -28,7 +28,8 @@ HEADERS = [os.path.join(CSRC, f) for f in ("fp8bq_internal.h", "fp8bq_device.cuh
                                                    "fp8bq_tile.cuh", "fp8bq_fp4.h",
                                                    "fp8bq_fp4_device.cuh")] + [
     os.path.join(ROOT, "include", "fp8bq.h")]
-# the Python binding's call module (C, no CUDA code of its own)
+# the Python binding's call module (C, no CUDA code of its own); built at the first
+# 4-bit call, since nothing else needs it, nor a C compiler and Python's headers
 CALLS_SOURCE = os.path.join(CSRC, "fp8bq_calls.c")
 CALLS = os.path.join(PKG, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 LIB = os.path.join(PKG, "libfp8bq.so")
@@ -76,8 +77,6 @@ def build(force: bool = False, verbose_ptxas: bool = False, out: str | None = No
     are extra -D tuning constants; ``checked`` builds the bounds-checked
     library (default path ``libfp8bq_checked.so``)."""
     lib = out or (LIB_CHECKED if checked else LIB)
-    if out is None:
-        build_calls(force)
     if checked:
         defines = (*defines, "FP8BQ_CHECKED=1")
     if out is None and not force and not verbose_ptxas and \
@@ -100,4 +99,8 @@ if __name__ == "__main__":
     ap.add_argument("--checked", action="store_true")
     a = ap.parse_args()
     print(build(force=a.force, verbose_ptxas=a.verbose_ptxas, checked=a.checked))
+    try:
+        print(build_calls(force=a.force))
+    except (OSError, subprocess.SubprocessError) as e:  # the Python calls do without
+        print(f"{CALLS}: not built: {e}", file=sys.stderr)
     sys.exit(0)
