@@ -191,6 +191,10 @@ def lib() -> ctypes.CDLL:
             L.fp8bq_set_pdl.restype = i32
             L.fp8bq_get_pdl.argtypes = []
             L.fp8bq_get_pdl.restype = i32
+            L.fp8bq_set_pdl_min_us.argtypes = [ctypes.c_double]
+            L.fp8bq_set_pdl_min_us.restype = i32
+            L.fp8bq_get_pdl_min_us.argtypes = []
+            L.fp8bq_get_pdl_min_us.restype = ctypes.c_double
             L.fp8bq_path_for.argtypes = [ctypes.POINTER(fp8bq_desc)]
             L.fp8bq_path_for.restype = i32
             L.fp8bq_launch_count.argtypes = [ctypes.POINTER(fp8bq_desc), i32]
@@ -218,6 +222,12 @@ def lib() -> ctypes.CDLL:
             L.fp8bq_fp4_matmul.restype = i32
             L.fp8bq_fp4_gated_matmul.argtypes = [vp, vp]
             L.fp8bq_fp4_gated_matmul.restype = i32
+            L.fp8bq_fp4_plan.argtypes = [ctypes.POINTER(fp8bq_fp4_matmul_desc), i32,
+                                         ctypes.POINTER(i32), ctypes.POINTER(i32)]
+            L.fp8bq_fp4_plan.restype = i32
+            # A call through Python takes about 9 us.  With the launch overlap for every
+            # call, one token's product takes 1.6 us more of them.
+            L.fp8bq_set_pdl_min_us(6.5)
             _lib = L
     return _lib
 
@@ -328,6 +338,13 @@ def fp8bq_fp4_gated_matmul(desc: fp8bq_fp4_matmul_desc, stream=None) -> int:
     return lib().fp8bq_fp4_gated_matmul(ctypes.byref(desc), _stream(stream))
 
 
+def fp8bq_fp4_plan(desc: fp8bq_fp4_matmul_desc, gated: bool = False) -> tuple[int, int, int]:
+    """``fp8bq_fp4_plan`` of the C ABI: (status, tokens, overlap)."""
+    t, o = ctypes.c_int(-1), ctypes.c_int(-1)
+    st = lib().fp8bq_fp4_plan(ctypes.byref(desc), int(gated), ctypes.byref(t), ctypes.byref(o))
+    return st, t.value, o.value
+
+
 def fp8bq_status_string(status: int) -> str:
     return lib().fp8bq_status_string(status).decode()
 
@@ -354,6 +371,14 @@ def fp8bq_set_pdl(enable: int) -> int:
 
 def fp8bq_get_pdl() -> int:
     return lib().fp8bq_get_pdl()
+
+
+def fp8bq_set_pdl_min_us(us: float) -> int:
+    return lib().fp8bq_set_pdl_min_us(us)
+
+
+def fp8bq_get_pdl_min_us() -> float:
+    return lib().fp8bq_get_pdl_min_us()
 
 
 def fp8bq_path_for(desc: fp8bq_desc) -> int:

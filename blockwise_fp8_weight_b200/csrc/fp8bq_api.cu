@@ -28,6 +28,7 @@ std::atomic<int> g_path{FP8BQ_PATH_AUTO};
 std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
 std::atomic<uint32_t> g_inject{0};
 std::atomic<int> g_pdl{1};
+std::atomic<double> g_pdl_min_us{0.0};
 
 int esize_of(int32_t dtype) { return dtype == FP8BQ_BF16 ? 2 : 4; }
 
@@ -935,6 +936,7 @@ bool fp8bq::pdl_enabled() { return g_pdl.load(std::memory_order_relaxed) != 0; }
 // What the 4-bit entry points (fp8bq_fp4_api.cu) share with these.
 fp8bq_status fp8bq::device_status() { return check_device(); }
 uint64_t fp8bq::wait_limit() { return g_wait_limit_ns.load(); }
+double fp8bq::pdl_min_us() { return g_pdl_min_us.load(std::memory_order_relaxed); }
 uint32_t fp8bq::inject_flags() { return g_inject.load(); }
 uint64_t fp8bq::checked_extent(uint64_t bytes) { return checked_out_extent(bytes); }
 PFN_cuTensorMapEncodeTiled_v12000 fp8bq::tensor_map_encoder() { return encode_fn(); }
@@ -1065,6 +1067,14 @@ fp8bq_status fp8bq_set_pdl(int enable) {
 }
 
 int fp8bq_get_pdl(void) { return g_pdl.load(); }
+
+fp8bq_status fp8bq_set_pdl_min_us(double us) {
+    if (!(us >= 0.0)) return FP8BQ_ERR_ARG;
+    g_pdl_min_us.store(us);
+    return FP8BQ_OK;
+}
+
+double fp8bq_get_pdl_min_us(void) { return g_pdl_min_us.load(); }
 
 int fp8bq_path_for(const fp8bq_desc *desc) {
     if (desc == nullptr) return -1;

@@ -18,11 +18,14 @@ uint64_t checked_extent(uint64_t);  // an output's extent for the bounds checks
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Whether a call that takes the device about `us` microseconds is launched
-// with programmatic stream serialization.  The attribute costs the host 1.6 us
-// a launch (4.2 against 2.6 measured), and saves the device 2 to 3:
-// it is left out where the host, at about 9 us a call through the Python
-// binding, is the slower side of the two anyway, outside a graph.  (515 tokens
-// against 1000 x 4100, about 8 us: 12.3 us a call without it, 9.6 with.)
+// with programmatic stream serialization: if it is on, unless the call is
+// shorter than pdl_min_us() and outside a graph.  The attribute costs the host
+// 1.6 us a launch (4.2 against 2.6 measured) and saves the device 2 to 3, so a
+// caller who needs longer for a call than the device does gains by leaving it
+// out.  (515 tokens against 1000 x 4100, about 8 us, through the Python binding:
+// 12.3 us a call without it, 9.6 with; one token against 6144 x 4096 in a loop of
+// C calls: 8.9 without, 6.5 with.)
+double pdl_min_us();                // fp8bq_set_pdl_min_us
 bool fp4_overlap(cudaStream_t st, double us);
 
 // ------------------------------------------------------------------ layout

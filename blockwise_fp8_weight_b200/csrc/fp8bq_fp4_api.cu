@@ -12,7 +12,7 @@ using namespace fp8bq;
 
 bool fp8bq::fp4_overlap(cudaStream_t st, double us) {
     if (!pdl_enabled()) return false;
-    if (us > 6.5) return true;
+    if (us >= pdl_min_us()) return true;
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) {
         cudaGetLastError();
@@ -285,9 +285,18 @@ bool map_scales(const Mat &m, const fp8bq_fp4_matmul_desc &D, CUtensorMap *out) 
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStream_t stream) {
-    if (desc == nullptr) return FP8BQ_ERR_NULL;
-    const fp8bq_fp4_matmul_desc &D = *desc;
+// A product that passed its checks, and how it is launched.
+struct Product {
+    Mat mats[3];
+    __int128 out_bytes;
+    int64_t obs, kb, stages;
+    int store_align;
+    int tokens;  // as from fp4_choose; -1: nothing to do
+    double us;
+};
+
+fp8bq_status plan_product(const fp8bq_fp4_matmul_desc &D, bool gated, Product *P) {
+    P->tokens = -1;
     if (!dtype_ok(D.dtype_out)) return FP8BQ_ERR_DTYPE;
     if (!format_ok(D.format)) return FP8BQ_ERR_ARG;
     if (D.M < 0 || D.N < 0 || D.batch < 0 || D.K < 1 || D.ld_out < D.N || D.M > kMaxDim ||
@@ -298,15 +307,15 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     if (((__int128)(D.M + 15) / 16) * ((D.N + 127) / 128) * D.batch >= (1ll << 31))
         return FP8BQ_ERR_SHAPE;
     const int es = esize_of(D.dtype_out);
-    const int64_t obs = D.batch > 1 ? D.out_batch_stride : 0;
+    const int64_t obs = P->obs = D.batch > 1 ? D.out_batch_stride : 0;
     if (obs < 0) return FP8BQ_ERR_SHAPE;
     if (D.out == nullptr) return FP8BQ_ERR_NULL;
     if ((uintptr_t)D.out % es || (uintptr_t)D.rows % 4) return FP8BQ_ERR_ALIGN;
-    const __int128 out_bytes =
+    const __int128 out_bytes = P->out_bytes =
         ((__int128)(D.batch - 1) * obs + (__int128)(D.M - 1) * D.ld_out + D.N) * es;
     if (out_bytes > kMaxBytes) return FP8BQ_ERR_SHAPE;
     if (D.batch > 1 && obs < (D.M - 1) * D.ld_out + D.N) return FP8BQ_ERR_OVERLAP;
-    Mat mats[3];
+    Mat *mats = P->mats;
     const int n = gated ? 3 : 2;
     const uintptr_t out_lo = (uintptr_t)D.out, out_hi = out_lo + (uintptr_t)out_bytes;
     auto in_out = [&](const void *q, __int128 bytes) {
@@ -322,20 +331,30 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
                    in_out(o.tensor_scale, mats[i].t_bytes);
     }
     if (overlap) return FP8BQ_ERR_OVERLAP;
-    const fp8bq_status sd = device_status();
-    if (sd != FP8BQ_OK) return sd;
-
-    const int64_t kb = fp4_row_bytes(D.K), stages = (kb + 127) / 128;
-    int store_align = es;
+    P->kb = fp4_row_bytes(D.K);
+    P->stages = (P->kb + 127) / 128;
+    P->store_align = es;
     for (int a : {4, 8, 16, 32})
         if ((uintptr_t)D.out % a == 0 && D.ld_out * es % a == 0 && obs * es % a == 0)
-            store_align = a;
-    double us = 0;
-    const int tokens = fp4_choose(D.M, D.N, stages, D.batch, gated, fp4_staged(store_align, es), &us);
-    const bool wide = tokens == 0;
+            P->store_align = a;
+    P->tokens = fp4_choose(D.M, D.N, P->stages, D.batch, gated, fp4_staged(P->store_align, es), &P->us);
+    return FP8BQ_OK;
+}
+
+fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStream_t stream) {
+    if (desc == nullptr) return FP8BQ_ERR_NULL;
+    const fp8bq_fp4_matmul_desc &D = *desc;
+    Product P;
+    const fp8bq_status s = plan_product(D, gated, &P);
+    if (s != FP8BQ_OK || P.tokens < 0) return s;
+    const fp8bq_status sd = device_status();
+    if (sd != FP8BQ_OK) return sd;
+    const Mat *mats = P.mats;
+    const int n = gated ? 3 : 2;
+    const bool wide = P.tokens == 0;
     Fp4MmParams p;
     std::memset(&p, 0, sizeof p);
-    bool ok = map_codes(mats[0], D, wide ? 128 : tokens, &p.x) && map_scales(mats[0], D, &p.xs);
+    bool ok = map_codes(mats[0], D, wide ? 128 : P.tokens, &p.x) && map_scales(mats[0], D, &p.xs);
     for (int i = 1; ok && i < n; ++i)
         ok = map_codes(mats[i], D, 128, &p.w[i - 1]) && map_scales(mats[i], D, &p.ws[i - 1]);
     if (!ok) return FP8BQ_ERR_DEVICE;
@@ -348,28 +367,28 @@ fp8bq_status run_matmul(const fp8bq_fp4_matmul_desc *desc, bool gated, cudaStrea
     p.out = D.out;
     p.rows = D.rows;
     p.ldo = D.ld_out;
-    p.obs = obs;
+    p.obs = P.obs;
     p.wait_limit_ns = wait_limit();
     p.M = (int32_t)D.M;
     p.N = (int32_t)D.N;
     p.batch = (int32_t)D.batch;
-    p.stages_k = (int32_t)stages;
-    p.mma_k = (int32_t)((kb + 31) / 32);
+    p.stages_k = (int32_t)P.stages;
+    p.mma_k = (int32_t)((P.kb + 31) / 32);
     p.split = 1;
-    p.store_align = store_align;
+    p.store_align = P.store_align;
     for (int i = 0; i < n; ++i)  // a stack stride of 0: one matrix for the whole stack
         p.moves |= (mats[i].cbs ? 1u : 0u) << (2 * i) | (mats[i].sbs ? 2u : 0u) << (2 * i);
-    p.overlap = fp4_overlap(stream, us);
+    p.overlap = fp4_overlap(stream, P.us);
     p.inject = inject_flags();
 #if FP8BQ_CHECKED
-    p.out_bytes = checked_extent((uint64_t)out_bytes);
+    p.out_bytes = checked_extent((uint64_t)P.out_bytes);
     p.rows_bytes = (uint64_t)D.batch * 4;
     p.xt_bytes = (uint64_t)mats[0].t_bytes;
     for (int i = 1; i < n; ++i) p.wt_bytes[i - 1] = (uint64_t)mats[i].t_bytes;
 #endif
     const bool bf16 = D.dtype_out == FP8BQ_BF16;
     if ((wide ? launch_fp4_mm_wide(p, D.format, gated, bf16, stream)
-              : launch_fp4_mm_narrow(p, D.format, gated, bf16, tokens, stream)) != cudaSuccess) {
+              : launch_fp4_mm_narrow(p, D.format, gated, bf16, P.tokens, stream)) != cudaSuccess) {
         cudaGetLastError();
         return FP8BQ_ERR_DEVICE;
     }
@@ -424,6 +443,16 @@ fp8bq_status fp8bq_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, i
                                (int32_t)format},
                               stream);
     });
+}
+
+fp8bq_status fp8bq_fp4_plan(const fp8bq_fp4_matmul_desc *desc, int gated, int *tokens, int *overlap) {
+    if (desc == nullptr) return FP8BQ_ERR_NULL;
+    Product P;
+    const fp8bq_status s = plan_product(*desc, gated != 0, &P);
+    if (s != FP8BQ_OK) return s;
+    if (tokens) *tokens = P.tokens;
+    if (overlap) *overlap = P.tokens < 0 ? -1 : pdl_enabled() && P.us >= pdl_min_us();
+    return FP8BQ_OK;
 }
 
 fp8bq_status fp8bq_fp4_matmul(const fp8bq_fp4_matmul_desc *desc, cudaStream_t stream) {

@@ -372,6 +372,17 @@ FP8BQ_API fp8bq_status fp8bq_fp4_matmul(const fp8bq_fp4_matmul_desc *desc, cudaS
 FP8BQ_API fp8bq_status fp8bq_fp4_gated_matmul(const fp8bq_fp4_matmul_desc *desc,
                                               cudaStream_t stream);
 
+/*
+ * How a product (gated: fp8bq_fp4_gated_matmul) would be launched: host only,
+ * launches nothing.  *tokens: the width in tokens of the few-token kernel's
+ * tiles (16, 32, 64, 128 or 256), or 0 for the many-token kernel; *overlap: 1
+ * if it would be launched with programmatic stream serialization outside a
+ * capture, else 0.  Both -1 where there is nothing to do.  Either pointer may be
+ * NULL.  Argument errors as from the call.
+ */
+FP8BQ_API fp8bq_status fp8bq_fp4_plan(const fp8bq_fp4_matmul_desc *desc, int gated, int *tokens,
+                                      int *overlap);
+
 /* Human-readable name of a status code (static string, never NULL). */
 FP8BQ_API const char *fp8bq_status_string(fp8bq_status status);
 
@@ -460,6 +471,18 @@ FP8BQ_API int fp8bq_launch_count(const fp8bq_desc *desc_table, int n_tensors);
  */
 FP8BQ_API fp8bq_status fp8bq_set_pdl(int enable);
 FP8BQ_API int fp8bq_get_pdl(void);
+
+/*
+ * 4-bit calls (fp8bq_fp4_*) that would take the device less than `us`
+ * microseconds, by the library's estimate, are launched plainly although
+ * fp8bq_set_pdl is on, except into a graph that is being captured.  For
+ * callers whose own time a call is the longer one: the overlap costs the host
+ * 1.6 us a launch.  Process-wide; 0, the default, leaves none out; negative or
+ * NaN: FP8BQ_ERR_ARG.  The Python package, which needs about 9 us a call, sets
+ * 6.5 when it loads the library.
+ */
+FP8BQ_API fp8bq_status fp8bq_set_pdl_min_us(double us);
+FP8BQ_API double fp8bq_get_pdl_min_us(void);
 
 /*
  * Fault-injection and wait-limit knobs for tests (host side; process-wide).
