@@ -1018,8 +1018,9 @@ cudaError_t launch_clusters(K kern, dim3 grid, unsigned threads, unsigned cluste
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// Clusters of each size that fit on the device at once (cluster sizes the
-// device cannot run count as 0).
+// Clusters of each size that fit on the device at once (a size that the device
+// cannot run counts as 0).
+constexpr int kSplits[] = {2, 3, 4, 6, 8};  // 5 and 7 measured no better than 4 and 6
 struct ClusterFit {
     cudaError_t attr = cudaSuccess;
     int n[9] = {};
@@ -1032,7 +1033,7 @@ template <typename K>
 ClusterFit cluster_fit(K kern, unsigned threads, int smem, int per_sm) {
     ClusterFit f;
     f.attr = set_smem(kern, smem);
-    for (unsigned c = 1; f.attr == cudaSuccess && c <= 8; ++c) {
+    auto ask = [&](int c) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = 8 * c;
         cfg.blockDim = threads;
@@ -1043,12 +1044,21 @@ ClusterFit cluster_fit(K kern, unsigned threads, int smem, int per_sm) {
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&f.n[c], kern, &cfg) != cudaSuccess) {
-            cudaGetLastError();
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&f.n[c], kern, &cfg);
+        if (e != cudaSuccess) {
             f.n[c] = 0;
+            // any other failure is the call's: with fewer clusters it would add up
+            // other parts
+            if (c == 1 || (e != cudaErrorInvalidClusterSize && e != cudaErrorInvalidConfiguration))
+                f.attr = e;
+            else
+                cudaGetLastError();
         }
         f.n[c] *= per_sm;
-    }
+    };
+    if (f.attr == cudaSuccess) ask(1);
+    for (int c : kSplits)
+        if (f.attr == cudaSuccess) ask(c);
     if (f.attr == cudaSuccess && f.n[1] < 1) f.attr = cudaErrorInvalidConfiguration;
     return f;
 }
@@ -1058,14 +1068,16 @@ cudaError_t narrow(const Fp4MmParams &p0, cudaStream_t st) {
     using S = Narrow<FMT, GATED, NT>;
     auto kern = k_fp4_narrow<FMT, GATED, BF16, NT>;
     static PerDevice<ClusterFit> setup;
-    const ClusterFit fit = setup.get([&] { return cluster_fit(kern, S::kThreads, S::kSmem, S::kTwo ? 2 : 1); });
+    const ClusterFit fit =
+        setup.get([&] { return cluster_fit(kern, S::kThreads, S::kSmem, S::kTwo ? 2 : 1); },
+                  [](const ClusterFit &f) { return f.attr == cudaSuccess; });
     if (fit.attr != cudaSuccess) return fit.attr;
     Fp4MmParams p = p0;
     const int64_t tiles = (int64_t)((p.N + 127) / 128) * ((p.M + NT - 1) / NT) * p.batch;
     // The largest of these cluster sizes with which every tile runs at once
-    // and each CTA has a stage; 5 and 7 measured no better than 4 and 6.
+    // and each CTA has a stage.
     p.split = 1;
-    for (int c : {2, 3, 4, 6, 8})
+    for (int c : kSplits)
         if (tiles <= fit.n[c] && c <= p.stages_k) p.split = c;
     const int64_t clusters = p.split > 1 || tiles < fit.n[1] ? tiles : fit.n[1];
     return launch_clusters(kern, dim3((unsigned)(clusters * p.split)), S::kThreads,
@@ -1100,7 +1112,8 @@ cudaError_t wide(const Fp4MmParams &p, cudaStream_t st) {
     using S = Wide<FMT>;
     auto kern = k_fp4_wide<FMT, GATED, BF16, ALIGN>;
     static PerDevice<cudaError_t> setup;
-    const cudaError_t e = setup.get([&] { return set_smem(kern, S::kSmem); });
+    const cudaError_t e = setup.get([&] { return set_smem(kern, S::kSmem); },
+                                    [](cudaError_t r) { return r == cudaSuccess; });
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)((p.M + 255) / 256) * ((p.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256)) *
                           p.batch;
@@ -1176,7 +1189,7 @@ int fp4_choose(int64_t M, int64_t N, int64_t stages, int64_t batch, bool gated, 
         const double once = c.tokens == 0 ? sms / 2 : two ? 2 * sms : sms;
         double share = (double)stages;  // stages of a CTA where a cluster splits K
         if (c.tokens)
-            for (int s : {2, 3, 4, 6, 8})  // clusters of more than two leave some SMs out
+            for (int s : kSplits)  // clusters of more than two leave some SMs out
                 if (s <= stages && tiles * s <= once * (s == 2 ? 1.0 : s == 8 ? 0.82 : 0.9))
                     share = (double)((stages + s - 1) / s);
         const double rounds = (double)(int64_t)((tiles + once - 1) / once);

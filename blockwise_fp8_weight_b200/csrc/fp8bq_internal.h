@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 
 #ifndef FP8BQ_CHECKED
@@ -29,20 +30,35 @@ inline int current_device() {
     return dev;
 }
 
-// A value made once per device (devices beyond kMaxDevices: made on every call).
+// A value made once per device (devices beyond kMaxDevices: made on every
+// call).  One that is not `good` is returned but not kept, so that a set-up
+// that failed for a passing reason (no memory to load the kernel) is made again
+// by the next call.
 template <typename T>
 class PerDevice {
   public:
     template <typename F>
     T get(F &&make) {
+        return get(make, [](const T &) { return true; });
+    }
+    template <typename F, typename G>
+    T get(F &&make, G &&good) {
         const int dev = current_device();
         if (dev < 0 || dev >= kMaxDevices) return make();
-        std::call_once(once_[dev], [&] { val_[dev] = make(); });
-        return val_[dev];
+        if (made_[dev].load(std::memory_order_acquire)) return val_[dev];
+        std::lock_guard<std::mutex> lock(mu_);
+        if (made_[dev].load(std::memory_order_relaxed)) return val_[dev];
+        const T v = make();
+        if (good(v)) {
+            val_[dev] = v;
+            made_[dev].store(true, std::memory_order_release);
+        }
+        return v;
     }
 
   private:
-    std::once_flag once_[kMaxDevices];
+    std::mutex mu_;
+    std::atomic<bool> made_[kMaxDevices] = {};
     T val_[kMaxDevices];
 };
 

@@ -492,7 +492,7 @@ cudaError_t launch_vector_h(const DescPack<MAXD> &p, cudaStream_t st) {
     constexpr size_t smem = (size_t)S * V * CTA * 16;
     auto kern = k_vector<ESIZE, TEAM, V, CTA, G, MAXD, HALVES, S>;
     static PerDevice<KernelSetup> setup;
-    const KernelSetup ks = setup.get([&] { return setup_kernel(kern, CTA, smem); });
+    const KernelSetup ks = setup.get([&] { return setup_kernel(kern, CTA, smem); }, setup_done);
     if (ks.attr != cudaSuccess) return ks.attr;
     // short launches (fewer than FP8BQ_VEC_SHORT_TILES tiles per resident
     // team) take FP8BQ_VEC_WAVES_SHORT waves

@@ -229,6 +229,8 @@ struct KernelSetup {
     int occ;
 };
 
+inline bool setup_done(const KernelSetup &s) { return s.attr == cudaSuccess; }
+
 template <typename K>
 inline KernelSetup setup_kernel(K kernel, int threads, size_t smem) {
     KernelSetup s{cudaSuccess, 1};

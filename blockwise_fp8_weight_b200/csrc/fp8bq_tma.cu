@@ -468,7 +468,7 @@ cudaError_t launch_tma_e(const TmaPack<MAXD> &p, cudaStream_t st) {
     auto kern = k_tma<ESIZE, STAGES, MODE, MAXD, EF>;
     static PerDevice<KernelSetup> setup;
     const KernelSetup ks =
-        setup.get([&] { return setup_kernel(kern, 32 + kTmaConsumerThreads, smem); });
+        setup.get([&] { return setup_kernel(kern, 32 + kTmaConsumerThreads, smem); }, setup_done);
     if (ks.attr != cudaSuccess) return ks.attr;
     const unsigned grid = grid_for(p.p.total_tiles, 1, ks.occ * FP8BQ_TMA_WAVES);
     return launch_kernel(kern, grid, 32 + kTmaConsumerThreads, smem, st, p);
@@ -489,7 +489,7 @@ cudaError_t launch_tma_pair_e(const TmaPack<MAXD> &p, cudaStream_t st) {
     auto kern = k_tma_pair<S, MAXD, EF>;
     static PerDevice<KernelSetup> setup;
     const KernelSetup ks =
-        setup.get([&] { return setup_kernel(kern, 32 + kTmaConsumerThreads, smem); });
+        setup.get([&] { return setup_kernel(kern, 32 + kTmaConsumerThreads, smem); }, setup_done);
     if (ks.attr != cudaSuccess) return ks.attr;
     const unsigned grid = grid_for(p.p.total_tiles, 1, ks.occ * FP8BQ_TMA_WAVES);
     return launch_kernel(kern, grid, 32 + kTmaConsumerThreads, smem, st, p);
