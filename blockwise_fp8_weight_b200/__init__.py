@@ -225,6 +225,8 @@ def lib() -> ctypes.CDLL:
             L.fp8bq_fp4_plan.argtypes = [ctypes.POINTER(fp8bq_fp4_matmul_desc), i32,
                                          ctypes.POINTER(i32), ctypes.POINTER(i32)]
             L.fp8bq_fp4_plan.restype = i32
+            L.fp8bq_debug_set_fp4_tokens.argtypes = [i32]
+            L.fp8bq_debug_set_fp4_tokens.restype = i32
             # A call through Python takes about 9 us.  With the launch overlap for every
             # call, one token's product takes 1.6 us more of them.
             L.fp8bq_set_pdl_min_us(6.5)
@@ -400,6 +402,10 @@ def fp8bq_debug_set_wait_limit_ns(ns: int) -> int:
 
 def fp8bq_debug_set_inject(flags: int) -> int:
     return lib().fp8bq_debug_set_inject(flags)
+
+
+def fp8bq_debug_set_fp4_tokens(tokens: int) -> int:
+    return lib().fp8bq_debug_set_fp4_tokens(tokens)
 
 
 def fp8bq_checked_build() -> int:

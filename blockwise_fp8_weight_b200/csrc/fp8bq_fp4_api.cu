@@ -3,6 +3,7 @@
 // kernel.  A tensor map is made for each call from its arguments (under a
 // microsecond each): nothing is kept from one call to the next.
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <vector>
 
@@ -295,6 +296,13 @@ struct Product {
     double us;
 };
 
+std::atomic<int> g_force_tokens{-1};  // fp8bq_debug_set_fp4_tokens
+
+// Whether tiles of that width (0: the many-token kernel) can compute M tokens.
+bool tokens_ok(int tokens, int64_t M, bool gated) {
+    return tokens == 0 || (tokens >= 64 ? tokens <= (gated ? 128 : 256) : M <= tokens);
+}
+
 fp8bq_status plan_product(const fp8bq_fp4_matmul_desc &D, bool gated, Product *P) {
     P->tokens = -1;
     if (!dtype_ok(D.dtype_out)) return FP8BQ_ERR_DTYPE;
@@ -338,6 +346,8 @@ fp8bq_status plan_product(const fp8bq_fp4_matmul_desc &D, bool gated, Product *P
         if ((uintptr_t)D.out % a == 0 && D.ld_out * es % a == 0 && obs * es % a == 0)
             P->store_align = a;
     P->tokens = fp4_choose(D.M, D.N, P->stages, D.batch, gated, fp4_staged(P->store_align, es), &P->us);
+    const int force = g_force_tokens.load(std::memory_order_relaxed);
+    if (force >= 0 && tokens_ok(force, D.M, gated)) P->tokens = force;
     return FP8BQ_OK;
 }
 
@@ -443,6 +453,15 @@ fp8bq_status fp8bq_fp4_dequantize(const uint8_t *codes, const uint8_t *scales, i
                                (int32_t)format},
                               stream);
     });
+}
+
+fp8bq_status fp8bq_debug_set_fp4_tokens(int tokens) {
+    for (int t : {-1, 0, 16, 32, 64, 128, 256})
+        if (t == tokens) {
+            g_force_tokens.store(tokens);
+            return FP8BQ_OK;
+        }
+    return FP8BQ_ERR_ARG;
 }
 
 fp8bq_status fp8bq_fp4_plan(const fp8bq_fp4_matmul_desc *desc, int gated, int *tokens, int *overlap) {

@@ -383,6 +383,16 @@ FP8BQ_API fp8bq_status fp8bq_fp4_gated_matmul(const fp8bq_fp4_matmul_desc *desc,
 FP8BQ_API fp8bq_status fp8bq_fp4_plan(const fp8bq_fp4_matmul_desc *desc, int gated, int *tokens,
                                       int *overlap);
 
+/*
+ * Force the kernel of the products that follow (process-wide; for tests, as
+ * fp8bq_set_path is for the quantizer): a tile width in tokens as
+ * fp8bq_fp4_plan reports it, 0 for the many-token kernel, -1 (the default) for
+ * the library's choice.  Products that the forced tiles cannot serve (16 and 32
+ * hold all tokens or none; gated tiles end at 128) take that choice.
+ * FP8BQ_ERR_ARG for any other value.
+ */
+FP8BQ_API fp8bq_status fp8bq_debug_set_fp4_tokens(int tokens);
+
 /* Human-readable name of a status code (static string, never NULL). */
 FP8BQ_API const char *fp8bq_status_string(fp8bq_status status);
 

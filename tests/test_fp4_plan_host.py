@@ -17,6 +17,7 @@ def _settings():
     yield
     fq.fp8bq_set_pdl(1)
     fq.fp8bq_set_pdl_min_us(6.5)
+    fq.fp8bq_debug_set_fp4_tokens(-1)
 
 
 def product(M, N, K, batch=1):
@@ -70,3 +71,18 @@ def test_plans_and_their_refusals():
     L = fq.lib()
     assert L.fp8bq_fp4_plan(None, 0, None, None) == fq.FP8BQ_ERR_NULL
     assert L.fp8bq_fp4_plan(product(1, 256, 512), 0, None, None) == fq.FP8BQ_OK
+
+
+def test_forced_kernels():
+    """A forced width is taken by every product it can serve."""
+    for bad in (-2, 1, 48, 512):
+        assert fq.fp8bq_debug_set_fp4_tokens(bad) == fq.FP8BQ_ERR_ARG
+    for M in (1, 16, 17, 32, 33, 700):
+        for gated in (False, True):
+            assert fq.fp8bq_debug_set_fp4_tokens(-1) == fq.FP8BQ_OK
+            own = fq.fp8bq_fp4_plan(product(M, 300, 512), gated)
+            for t in (0, 16, 32, 64, 128, 256):
+                assert fq.fp8bq_debug_set_fp4_tokens(t) == fq.FP8BQ_OK
+                serves = t == 0 or (M <= t if t < 64 else t <= (128 if gated else 256))
+                got = fq.fp8bq_fp4_plan(product(M, 300, 512), gated)
+                assert got[:2] == (fq.FP8BQ_OK, t if serves else own[1])
